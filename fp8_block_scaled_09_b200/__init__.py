@@ -15,6 +15,13 @@ Functions (names follow the C ABI without the ``fp8bq_`` prefix):
 * ``linear(x, qw, sw)``      -> BF16 [M, N], activation quantization fused into the call
 * ``kv_write_e4m3(k, v, loc, k_cache, v_cache)``  E4M3 unit-scale KV-cache write (in place)
 * ``silu_mul_quantize(gu)``  BF16 [M, 2I] gate|up -> (codes [M, I], FP32 [M, I/128])
+* ``rms_norm_quantize(x, weight, eps, residual)``  norm (+ residual) -> (codes, FP32 scales);
+  ``rms_norm(...)`` -> BF16
+* ``rope_inv_freq(rot_dim, base, scaling, ...)``  -> (FP32 frequencies, factor on cos and sin)
+* ``rope_kv_write_e4m3(qkv, positions, inv_freq, loc, k_cache, v_cache)``  rotated queries BF16;
+  rotated keys and values to the E4M3 cache (in place)
+* ``paged_attention(q, k_cache, v_cache, page_table, seq_lens, cu_q, ...)``  attention of new
+  tokens over the paged E4M3 cache -> BF16
 * ``nvfp4_quantize_weight(w)`` BF16 [N, K] -> (packed uint8 [N, K/2], E4M3 uint8 [N, K/16], FP32 [1])
 * ``nvfp4_gemm_a16(x, packed, sb, g)`` BF16 [M, K] x NVFP4 W -> BF16 [M, N]
 """
@@ -31,13 +38,17 @@ __all__ = [
     "workspace_size", "new_workspace", "workspace_init", "last_device_status",
     "launch_count", "status_string", "selftest_timeout", "OP_GEMM", "OP_LINEAR", "OP_GEMM_SILU",
     "LIB_PATH", "kv_write_e4m3", "silu_mul_quantize", "gemm_silu_mul_quantize",
-    "nvfp4_quantize_weight", "nvfp4_gemm_a16",
+    "nvfp4_quantize_weight", "nvfp4_gemm_a16", "rms_norm_quantize", "rms_norm", "rope_inv_freq",
+    "rope_kv_write_e4m3", "paged_attention", "attention_workspace_size", "new_attention_workspace",
+    "HEAD_DIM",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8bq.so")
 OP_GEMM = 0
 OP_LINEAR = 1
 OP_GEMM_SILU = 2
+HEAD_DIM = 128  # channels of a head in paged_attention
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 STATUS_NAMES = {
     0: "FP8BQ_OK", 1: "FP8BQ_ERR_INVALID_ARG", 2: "FP8BQ_ERR_UNSUPPORTED_SHAPE",
@@ -80,6 +91,14 @@ def lib() -> ctypes.CDLL:
         L.fp8bq_gemm_silu_mul_quantize.argtypes = [P, P, P, P, I, I, I, P, P, P, P, S, P]
         L.fp8bq_nvfp4_quantize_weight.argtypes = [P, I, I, P, P, P, P]
         L.fp8bq_nvfp4_gemm_a16.argtypes = [P, P, P, P, I, I, I, P, P]
+        F, D, N = ctypes.c_float, ctypes.c_double, ctypes.c_int
+        L.fp8bq_rms_norm_quantize.argtypes = [P, P, P, F, I, I, P, P, P, P, P]
+        L.fp8bq_rope_inv_freq.argtypes = [I, D, N, D, D, D, D, P, P]
+        L.fp8bq_rope_kv_write_e4m3.argtypes = [P, I, I, I, I, I, P, P, I, N, F, P, P, I, P, P, I, I, P]
+        L.fp8bq_paged_attention.argtypes = [P, I, P, P, I, I, P, I, I, I, P, P, I, I, I, I, I, F, N,
+                                            P, I, P, P, S, P]
+        L.fp8bq_paged_attention_workspace_size.argtypes = [I, I, I, I, I]
+        L.fp8bq_paged_attention_workspace_size.restype = S
         L.fp8bq_workspace_size.argtypes = [ctypes.c_int, I, I, I]
         L.fp8bq_workspace_size.restype = S
         L.fp8bq_workspace_init.argtypes = [P, S, P]
@@ -96,7 +115,9 @@ def lib() -> ctypes.CDLL:
                      "fp8bq_workspace_init", "fp8bq_last_device_status", "fp8bq_gemm_noalloc",
                      "fp8bq_selftest_timeout", "fp8bq_kv_write_e4m3", "fp8bq_silu_mul_quantize",
                      "fp8bq_gemm_silu_mul_quantize",
-                     "fp8bq_nvfp4_quantize_weight", "fp8bq_nvfp4_gemm_a16"):
+                     "fp8bq_nvfp4_quantize_weight", "fp8bq_nvfp4_gemm_a16",
+                     "fp8bq_rms_norm_quantize", "fp8bq_rope_inv_freq", "fp8bq_rope_kv_write_e4m3",
+                     "fp8bq_paged_attention"):
             getattr(L, name).restype = st
         _lib = L
         return L
@@ -374,4 +395,215 @@ def nvfp4_gemm_a16(x: torch.Tensor, packed: torch.Tensor, sb: torch.Tensor, g: t
     _need(out, torch.bfloat16, "out")
     _check(lib().fp8bq_nvfp4_gemm_a16(_ptr(x), _ptr(packed), _ptr(sb), _ptr(g), M, N, K, _ptr(out),
                                       _stream(x)), "fp8bq_nvfp4_gemm_a16")
+    return out
+
+
+# The calls below take several tensors of one device, which need not be the
+# current one: each is checked and the library is called with that device current.
+def _rows(t: torch.Tensor, cols: int, name: str, like: torch.Tensor) -> None:
+    """t: BF16 [rows of like, cols] with unit column stride (rows may be strided)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != like.shape[0] or t.shape[1] != cols:
+        raise ValueError(f"{name} must be BF16 [{like.shape[0]}, {cols}], got {tuple(t.shape)}")
+    if t.shape[0] > 1 and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    _on(t, name, like)
+
+
+def _on(t: torch.Tensor, name: str, like: torch.Tensor) -> None:
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+
+
+def _dense(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, like: torch.Tensor) -> None:
+    _need(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    _on(t, name, like)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _call(t: torch.Tensor, name: str, *args) -> None:
+    """Calls the library on t's device and its current stream (passed as the last argument)."""
+    f = getattr(lib(), name)
+    if t.get_device() == torch.cuda.current_device():
+        _check(f(*args, _stream(t)), name)
+    else:
+        with torch.cuda.device(t.device):
+            _check(f(*args, _stream(t)), name)
+
+
+def _norm(x, weight, eps, residual, residual_out, q, s, h) -> None:
+    _need(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be BF16 [M, K]")
+    M, K = x.shape
+    _dense(weight, torch.bfloat16, (K,), "weight", x)
+    if residual is not None:
+        _dense(residual, torch.bfloat16, (M, K), "residual", x)
+        if residual_out is None:
+            residual_out = residual
+        _dense(residual_out, torch.bfloat16, (M, K), "residual_out", x)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if h is not None:
+        _dense(h, torch.bfloat16, (M, K), "h", x)
+    _call(x, "fp8bq_rms_norm_quantize", _ptr(x), _ptr(residual), _ptr(weight), eps, M, K,
+          _ptr(residual_out), _ptr(q), _ptr(s), _ptr(h))
+
+
+def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                      residual: torch.Tensor | None = None,
+                      residual_out: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                      s: torch.Tensor | None = None,
+                      h: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """fp8bq_rms_norm_quantize: the group-128 quantization of the root-mean-square norm of
+    r = BF16(x + residual) -> (codes uint8 [M, K], scales FP32 [M, K/128]).  x, residual: BF16
+    [M, K]; weight: BF16 [K].  r goes to residual_out, or in place of residual when that is
+    not given.  Pass h (BF16 [M, K]) to also receive the norm itself."""
+    _need(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be BF16 [M, K]")
+    M, K = x.shape
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    if s is None:
+        s = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
+    q = _codes(q)
+    _dense(q, torch.uint8, (M, K), "q", x)
+    _dense(s, torch.float32, (M, K // 128), "s", x)
+    _norm(x, weight, eps, residual, residual_out, q, s, h)
+    return q, s
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+             residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+             h: torch.Tensor | None = None) -> torch.Tensor:
+    """fp8bq_rms_norm_quantize without codes: the BF16 norm of r = BF16(x + residual), e.g.
+    before the BF16 output head.  Arguments as rms_norm_quantize."""
+    if h is None:
+        h = torch.empty_like(x)
+    _norm(x, weight, eps, residual, residual_out, None, None, h)
+    return h
+
+
+def rope_inv_freq(rot_dim: int, base: float, scaling: str = "plain", factor: float = 1.0,
+                  old_context: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                  device=None) -> tuple[torch.Tensor, float]:
+    """fp8bq_rope_inv_freq: (FP32 frequencies [rot_dim / 2] on `device`, factor on cos and sin).
+    scaling: "plain", "linear", "ntk" or "yarn" ("yarn" also needs old_context)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    f = torch.empty(max(0, int(rot_dim) // 2), dtype=torch.float32)
+    m = ctypes.c_float()
+    _check(lib().fp8bq_rope_inv_freq(rot_dim, base, ROPE_SCALINGS[scaling], factor, old_context,
+                                     beta_fast, beta_slow, _ptr(f), ctypes.addressof(m)),
+           "fp8bq_rope_inv_freq")
+    return (f if device is None else f.to(device)), m.value
+
+
+def _caches(k_cache, v_cache, like):
+    k_cache, v_cache = _codes(k_cache), _codes(v_cache)
+    if k_cache.dim() != 2:
+        raise ValueError("k_cache and v_cache must be [num_slots, slot_bytes]")
+    _dense(k_cache, torch.uint8, tuple(k_cache.shape), "k_cache", like)
+    _dense(v_cache, torch.uint8, tuple(k_cache.shape), "v_cache", like)
+    return k_cache, v_cache
+
+
+def rope_kv_write_e4m3(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+                       loc: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       head_dim: int = HEAD_DIM, kv_heads: int | None = None,
+                       interleaved: bool = False, mscale: float = 1.0,
+                       q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """fp8bq_rope_kv_write_e4m3: rotates the query and key heads of the fused QKV output (BF16
+    [T, (q_heads + 2 kv_heads) head_dim], rows may be strided) by positions (int64 [T]) and
+    writes keys and values to slots loc (int64 [T], -1: padding) of the E4M3 caches (uint8 or
+    float8_e4m3fn [num_slots, slot_bytes]).  kv_heads defaults to slot_bytes / head_dim.
+    Returns the rotated queries q_out (BF16 [T, q_heads head_dim], new unless given; may be
+    qkv's own query columns)."""
+    if not qkv.is_cuda or qkv.dim() != 2:
+        raise ValueError("qkv must be a 2-D CUDA tensor")
+    _rows(qkv, qkv.shape[1], "qkv", qkv)
+    T, cols = qkv.shape
+    k_cache, v_cache = _caches(k_cache, v_cache, qkv)
+    if head_dim <= 0 or cols % head_dim:
+        raise ValueError("qkv columns must be a multiple of head_dim")
+    if kv_heads is None:
+        kv_heads = k_cache.shape[1] // head_dim
+    q_heads = cols // head_dim - 2 * kv_heads
+    if q_heads <= 0:
+        raise ValueError(f"qkv of {cols} columns has no query heads beside 2 x {kv_heads} kv heads")
+    _dense(positions, torch.int64, (T,), "positions", qkv)
+    _dense(loc, torch.int64, (T,), "loc", qkv)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be FP32 [rot_dim / 2]")
+    _dense(inv_freq, torch.float32, tuple(inv_freq.shape), "inv_freq", qkv)
+    if q_out is None:
+        q_out = torch.empty((T, q_heads * head_dim), dtype=torch.bfloat16, device=qkv.device)
+    _rows(q_out, q_heads * head_dim, "q_out", qkv)
+    _call(qkv, "fp8bq_rope_kv_write_e4m3", _ptr(qkv), _row_stride(qkv), T, q_heads, kv_heads,
+          head_dim, _ptr(positions), _ptr(inv_freq), 2 * inv_freq.numel(), int(interleaved), mscale,
+          _ptr(loc), _ptr(q_out), _row_stride(q_out), _ptr(k_cache),
+          _ptr(v_cache), k_cache.shape[0], k_cache.shape[1])
+    return q_out
+
+
+def attention_workspace_size(T: int, B: int, q_heads: int, kv_heads: int, max_q_len: int) -> int:
+    return int(lib().fp8bq_paged_attention_workspace_size(T, B, q_heads, kv_heads, max_q_len))
+
+
+def new_attention_workspace(T: int, B: int, q_heads: int, kv_heads: int, max_q_len: int,
+                            device) -> torch.Tensor:
+    """A zero-filled (initial-state) workspace for paged_attention of this batch."""
+    return torch.zeros(max(attention_workspace_size(T, B, q_heads, kv_heads, max_q_len), 256),
+                       dtype=torch.uint8, device=device)
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q: torch.Tensor,
+                    page_size: int, q_heads: int, kv_heads: int, max_q_len: int,
+                    scale: float | None = None, causal: bool = True,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """fp8bq_paged_attention: attention of the new tokens q (BF16 [T, q_heads 128], rows may be
+    strided) over the paged E4M3 caches (uint8 or float8_e4m3fn [num_slots, slot_bytes]) ->
+    BF16 [T, q_heads 128].  Sequence b has rows cu_q[b] .. cu_q[b+1] - 1 of q, seq_lens[b] cache
+    positions (its new tokens' among them) and pages page_table[b] (int32 [B, max_pages]; rows
+    may be strided); seq_lens int32 [B], cu_q int32 [B + 1].  scale defaults to 128^-1/2.  Pass
+    lse (FP32 [T, q_heads]) to also receive the log of the softmax's denominator.  Out-of-range
+    pages and lengths are reported through last_device_status()."""
+    if not q.is_cuda or q.dim() != 2:
+        raise ValueError("q must be a 2-D CUDA tensor")
+    _rows(q, q_heads * HEAD_DIM, "q", q)
+    T = q.shape[0]
+    k_cache, v_cache = _caches(k_cache, v_cache, q)
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise TypeError("page_table must be int32 [B, max_pages]")
+    _on(page_table, "page_table", q)
+    B, pages = page_table.shape
+    if B > 0 and pages > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table must have unit column stride")
+    _dense(seq_lens, torch.int32, (B,), "seq_lens", q)
+    _dense(cu_q, torch.int32, (B + 1,), "cu_q", q)
+    if out is None:
+        out = torch.empty((T, q_heads * HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+    _rows(out, q_heads * HEAD_DIM, "out", q)
+    if lse is not None:
+        _dense(lse, torch.float32, (T, q_heads), "lse", q)
+    if workspace is None:
+        workspace = new_attention_workspace(T, B, q_heads, kv_heads, max_q_len, q.device)
+    _on(workspace, "workspace", q)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _call(q, "fp8bq_paged_attention", _ptr(q), _row_stride(q), _ptr(k_cache), _ptr(v_cache),
+          k_cache.shape[0], k_cache.shape[1], _ptr(page_table),
+          page_table.stride(0) if B > 1 else max(pages, page_table.stride(0)), pages, page_size,
+          _ptr(seq_lens), _ptr(cu_q), B, T, q_heads, kv_heads, max_q_len,
+          HEAD_DIM ** -0.5 if scale is None else scale, int(causal), _ptr(out), _row_stride(out),
+          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size())
     return out

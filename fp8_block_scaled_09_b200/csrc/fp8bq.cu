@@ -23,6 +23,9 @@
 //   gemm_silu_mul_quantize -> M > 128: prefill::gemm_prefill_kernel<256, true, 16|32>
 //                       (gate/up GEMM whose epilogue quantizes silu(gate) * up);
 //                       smaller M: the decode GEMM, then silu_mul_quantize
+//   rms_norm_quantize -> rms_norm_kernel<V> (one CTA per row, V vectors per thread)
+//   rope_kv_write_e4m3 -> rope_kv_write_kernel
+//   paged_attention  -> attn::attention_simple_kernel
 //   linear           -> quantize_act into the workspace, then the gemm path; the
 //                       decode kernel then streams its first weight blocks while
 //                       the quantizer still runs (programmatic dependent launch)
@@ -31,12 +34,14 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <unordered_map>
 #include <utility>
 
+#include "attention.cuh"
 #include "fp8bq.h"
 #include "gemm_decode.cuh"
 #include "gemm_prefill.cuh"
@@ -45,6 +50,8 @@
 #include "kv_cache.cuh"
 #include "nvfp4.cuh"
 #include "quantize.cuh"
+#include "rms_norm.cuh"
+#include "rope.cuh"
 #include "silu_quant.cuh"
 
 namespace fp8bq {
@@ -651,6 +658,59 @@ size_t silu_ws_bytes(int64_t M, int64_t I) {
            round256(M * 2 * I * 2);
 }
 
+// ---------------------------------------------------------------- norm, rotary, attention
+
+constexpr int64_t kNormMaxK = int64_t(kNormMaxThreads) * 4 * 8;  // 4 vectors of 8 per thread
+constexpr int64_t kRopeMaxHeads = 1024;
+
+template <int V>
+cudaError_t launch_rms_norm_v(const DeviceInfo &d, const void *x, const void *residual,
+                              const void *weight, float eps, int64_t M, int64_t K,
+                              void *residual_out, uint8_t *q, float *s, void *h, cudaStream_t st) {
+    const int nvec = static_cast<int>(K / 8);
+    const int threads = ((nvec + V - 1) / V + 31) / 32 * 32;
+    const int64_t per_sm = std::max(1, 2048 / threads);
+    const int64_t grid = std::min<int64_t>(M, d.sm_count * per_sm);
+    return launch(rms_norm_kernel<V>, dim3(static_cast<unsigned>(grid)),
+                  dim3(static_cast<unsigned>(threads)), 0, st, static_cast<const uint4 *>(x),
+                  static_cast<const uint4 *>(residual), static_cast<const uint4 *>(weight), eps, M,
+                  nvec, static_cast<uint4 *>(residual_out), reinterpret_cast<uint2 *>(q), s,
+                  static_cast<uint4 *>(h));
+}
+
+cudaError_t launch_rms_norm(const DeviceInfo &d, const void *x, const void *residual,
+                            const void *weight, float eps, int64_t M, int64_t K, void *residual_out,
+                            uint8_t *q, float *s, void *h, cudaStream_t st) {
+    const int64_t nvec = K / 8;
+    if (nvec <= kNormMaxThreads)
+        return launch_rms_norm_v<1>(d, x, residual, weight, eps, M, K, residual_out, q, s, h, st);
+    if (nvec <= 2 * kNormMaxThreads)
+        return launch_rms_norm_v<2>(d, x, residual, weight, eps, M, K, residual_out, q, s, h, st);
+    return launch_rms_norm_v<4>(d, x, residual, weight, eps, M, K, residual_out, q, s, h, st);
+}
+
+// Cache positions of one sequence: 32-bit in the kernels, with room for a tile.
+constexpr int64_t kMaxContext = int64_t(1) << 30;
+constexpr int64_t kMaxBatch = 65536;
+
+fp8bq_status check_attention(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads,
+                             int64_t max_q_len) {
+    if (T < 0 || B < 0 || q_heads <= 0 || kv_heads <= 0 || max_q_len < 0 ||
+        (T > 0 && B > 0 && max_q_len == 0))
+        return FP8BQ_ERR_INVALID_ARG;
+    if (q_heads % kv_heads != 0 || q_heads > 1024 || T > kMaxDim / 1024 || B > kMaxBatch)
+        return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    return FP8BQ_OK;
+}
+
+size_t attention_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+
+fp8bq_status launch_attention(const DeviceInfo &d, const attn::Args &a, void *, cudaStream_t st) {
+    return from_cuda(launch(attn::attention_simple_kernel,
+                            dim3(static_cast<unsigned>(a.T * a.q_heads)),
+                            dim3(32 * attn::kSimpleWarps), 0, st, a, d.status));
+}
+
 }  // namespace
 }  // namespace fp8bq
 
@@ -780,6 +840,188 @@ fp8bq_status fp8bq_silu_mul_quantize(const void *gu_bf16, int64_t M, int64_t I, 
                             dim3(kSiluThreads), 0, static_cast<cudaStream_t>(stream),
                             static_cast<const uint4 *>(gu_bf16), M, I,
                             reinterpret_cast<uint2 *>(q_e4m3), s, static_cast<uint4 *>(h_bf16)));
+}
+
+fp8bq_status fp8bq_rms_norm_quantize(const void *x_bf16, const void *residual_bf16,
+                                     const void *weight_bf16, float eps, int64_t M, int64_t K,
+                                     void *residual_out_bf16, uint8_t *q_e4m3, float *s,
+                                     void *h_bf16, void *stream) {
+    fp8bq_status st = check_mk(M, K);
+    if (st != FP8BQ_OK) return st;
+    if (K > kNormMaxK) return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return FP8BQ_ERR_INVALID_ARG;
+    // codes and scales come together; one output at least; a residual's sum is
+    // always stored, and only then
+    if ((q_e4m3 == nullptr) != (s == nullptr) || (q_e4m3 == nullptr && h_bf16 == nullptr && M > 0) ||
+        (residual_bf16 == nullptr) != (residual_out_bf16 == nullptr))
+        return FP8BQ_ERR_INVALID_ARG;
+    if (M == 0) return FP8BQ_OK;
+    if (!x_bf16 || !weight_bf16) return FP8BQ_ERR_INVALID_ARG;
+    if (!aligned16(x_bf16) || !aligned16(residual_bf16) || !aligned16(weight_bf16) ||
+        !aligned16(residual_out_bf16) || !aligned16(q_e4m3) || !aligned16(s) || !aligned16(h_bf16))
+        return FP8BQ_ERR_MISALIGNED;
+    const DeviceInfo *d = device_info();
+    if (!d) return FP8BQ_ERR_NO_DEVICE;
+    return from_cuda(launch_rms_norm(*d, x_bf16, residual_bf16, weight_bf16, eps, M, K,
+                                     residual_out_bf16, q_e4m3, s, h_bf16,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+fp8bq_status fp8bq_rope_inv_freq(int64_t rot_dim, double base, fp8bq_rope_scaling scaling,
+                                 double factor, double old_context, double beta_fast,
+                                 double beta_slow, float *inv_freq, float *mscale) {
+    if (rot_dim <= 0 || rot_dim % 2 != 0 || rot_dim > kMaxDim) return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    if (!inv_freq || !mscale || !(base > 1.0) || std::isinf(base)) return FP8BQ_ERR_INVALID_ARG;
+    if (scaling < FP8BQ_ROPE_PLAIN || scaling > FP8BQ_ROPE_YARN) return FP8BQ_ERR_INVALID_ARG;
+    if (scaling != FP8BQ_ROPE_PLAIN && (!(factor >= 1.0) || std::isinf(factor)))
+        return FP8BQ_ERR_INVALID_ARG;
+    if (scaling == FP8BQ_ROPE_YARN && (!(old_context > 0.0) || std::isinf(old_context) ||
+                                       !(beta_slow > 0.0) || !(beta_fast > beta_slow) ||
+                                       std::isinf(beta_fast)))
+        return FP8BQ_ERR_INVALID_ARG;
+    const double R = static_cast<double>(rot_dim);
+    if (scaling == FP8BQ_ROPE_NTK && rot_dim > 2) base *= std::pow(factor, R / (R - 2.0));
+    for (int64_t i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * static_cast<double>(i) / R);
+        if (scaling == FP8BQ_ROPE_LINEAR) f /= factor;
+        if (scaling == FP8BQ_ROPE_YARN) {
+            const double turns = old_context * f / 6.283185307179586477;
+            const double keep = std::min(1.0, std::max(0.0, std::log(turns / beta_slow) /
+                                                                std::log(beta_fast / beta_slow)));
+            f = f * keep + f / factor * (1.0 - keep);
+        }
+        inv_freq[i] = static_cast<float>(f);
+    }
+    *mscale = scaling == FP8BQ_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return FP8BQ_OK;
+}
+
+fp8bq_status fp8bq_rope_kv_write_e4m3(const void *qkv_bf16, int64_t row_stride, int64_t T,
+                                      int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                      const int64_t *positions, const float *inv_freq,
+                                      int64_t rot_dim, int interleaved, float mscale,
+                                      const int64_t *loc, void *q_out_bf16, int64_t q_stride,
+                                      uint8_t *k_cache, uint8_t *v_cache, int64_t num_slots,
+                                      int64_t slot_stride, void *stream) {
+    if (T < 0 || q_heads <= 0 || kv_heads <= 0 || num_slots < 0 || !std::isfinite(mscale))
+        return FP8BQ_ERR_INVALID_ARG;
+    if (head_dim <= 0 || head_dim % 16 != 0 || head_dim > 2 * kRopeMaxPairs || rot_dim <= 0 ||
+        rot_dim % 16 != 0 || rot_dim > head_dim || q_heads > kRopeMaxHeads ||
+        kv_heads > kRopeMaxHeads || T > kMaxDim)
+        return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    const int64_t q_width = q_heads * head_dim, kv_width = kv_heads * head_dim;
+    if (row_stride < q_width + 2 * kv_width || q_stride < q_width || slot_stride < kv_width)
+        return FP8BQ_ERR_INVALID_ARG;
+    if (row_stride % 8 != 0 || q_stride % 8 != 0 || slot_stride % 16 != 0)
+        return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    if (T > 0 && (row_stride > kMaxBytes / 2 / T || q_stride > kMaxBytes / 2 / T))
+        return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    if (num_slots > 0 && slot_stride > kMaxBytes / num_slots) return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return FP8BQ_OK;
+    if (!qkv_bf16 || !positions || !inv_freq || !loc || !q_out_bf16 || !k_cache || !v_cache)
+        return FP8BQ_ERR_INVALID_ARG;
+    if (q_out_bf16 == qkv_bf16 && q_stride != row_stride) return FP8BQ_ERR_INVALID_ARG;
+    if (!aligned16(qkv_bf16) || !aligned16(q_out_bf16) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || (reinterpret_cast<uintptr_t>(positions) & 7u) != 0 ||
+        (reinterpret_cast<uintptr_t>(loc) & 7u) != 0 ||
+        (reinterpret_cast<uintptr_t>(inv_freq) & 3u) != 0)
+        return FP8BQ_ERR_MISALIGNED;
+    const DeviceInfo *d = device_info();
+    if (!d) return FP8BQ_ERR_NO_DEVICE;
+    RopeArgs a = {};
+    a.qkv = static_cast<const uint16_t *>(qkv_bf16);
+    a.q_out = static_cast<uint16_t *>(q_out_bf16);
+    a.positions = positions;
+    a.loc = loc;
+    a.inv_freq = inv_freq;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.row_stride = row_stride;
+    a.q_stride = q_stride;
+    a.T = T;
+    a.num_slots = num_slots;
+    a.slot_stride = slot_stride;
+    a.mscale = mscale;
+    a.q_heads = static_cast<int>(q_heads);
+    a.kv_heads = static_cast<int>(kv_heads);
+    a.dim = static_cast<int>(head_dim);
+    a.rot = static_cast<int>(rot_dim);
+    a.interleaved = interleaved != 0;
+    a.tok = T >= static_cast<int64_t>(d->sm_count) * 16 ? kRopeMaxTok : 1;
+    return from_cuda(launch(rope_kv_write_kernel, dim3(static_cast<unsigned>((T + a.tok - 1) / a.tok)),
+                            dim3(kRopeThreads), 0, static_cast<cudaStream_t>(stream), a, d->status));
+}
+
+size_t fp8bq_paged_attention_workspace_size(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads,
+                                            int64_t max_q_len) {
+    if (check_attention(T, B, q_heads, kv_heads, max_q_len) != FP8BQ_OK || T == 0) return 0;
+    return attention_ws_bytes(T, B, q_heads, kv_heads, max_q_len);
+}
+
+fp8bq_status fp8bq_paged_attention(const void *q_bf16, int64_t q_stride, const uint8_t *k_cache,
+                                   const uint8_t *v_cache, int64_t num_slots, int64_t slot_stride,
+                                   const int32_t *page_table, int64_t table_stride,
+                                   int64_t max_pages, int64_t page_size, const int32_t *seq_lens,
+                                   const int32_t *cu_q, int64_t B, int64_t T, int64_t q_heads,
+                                   int64_t kv_heads, int64_t max_q_len, float scale, int causal,
+                                   void *out_bf16, int64_t out_stride, float *lse, void *workspace,
+                                   size_t ws_bytes, void *stream) {
+    fp8bq_status st = check_attention(T, B, q_heads, kv_heads, max_q_len);
+    if (st != FP8BQ_OK) return st;
+    if (num_slots < 0 || max_pages < 0 || table_stride < max_pages || !(scale > 0.0f) ||
+        std::isinf(scale))
+        return FP8BQ_ERR_INVALID_ARG;
+    const int64_t q_width = q_heads * attn::kDim, kv_width = kv_heads * attn::kDim;
+    if (q_stride < q_width || out_stride < q_width || slot_stride < kv_width)
+        return FP8BQ_ERR_INVALID_ARG;
+    int shift = 0;
+    while (shift < 20 && (int64_t(1) << shift) < page_size) ++shift;
+    if (page_size < 8 || (int64_t(1) << shift) != page_size) return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    if (q_stride % 8 != 0 || out_stride % 8 != 0 || slot_stride % 16 != 0 || num_slots > kMaxDim ||
+        max_pages > kMaxContext / page_size || table_stride > kMaxBytes / 4 / std::max<int64_t>(B, 1))
+        return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    if (T > 0 && (q_stride > kMaxBytes / 2 / T || out_stride > kMaxBytes / 2 / T))
+        return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    if (num_slots > 0 && slot_stride > kMaxBytes / num_slots) return FP8BQ_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0 || B == 0) return FP8BQ_OK;
+    if (!q_bf16 || !seq_lens || !cu_q || !out_bf16) return FP8BQ_ERR_INVALID_ARG;
+    // a cache or table of no slots or pages may be absent: every context is then empty
+    if ((num_slots > 0 && (!k_cache || !v_cache)) || (max_pages > 0 && !page_table))
+        return FP8BQ_ERR_INVALID_ARG;
+    if (!aligned16(q_bf16) || !aligned16(out_bf16) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens) |
+          reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(lse)) & 3u) != 0)
+        return FP8BQ_ERR_MISALIGNED;
+    const size_t need = attention_ws_bytes(T, B, q_heads, kv_heads, max_q_len);
+    if (need && (!workspace || ws_bytes < need)) return FP8BQ_ERR_WORKSPACE;
+    if (need && !aligned16(workspace)) return FP8BQ_ERR_MISALIGNED;
+    const DeviceInfo *d = device_info();
+    if (!d) return FP8BQ_ERR_NO_DEVICE;
+    attn::Args a = {};
+    a.q = static_cast<const uint16_t *>(q_bf16);
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.table = page_table;
+    a.seq_lens = seq_lens;
+    a.cu_q = cu_q;
+    a.out = static_cast<uint16_t *>(out_bf16);
+    a.lse = lse;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.table_stride = table_stride;
+    a.slot_stride = slot_stride;
+    a.T = T;
+    a.num_pages = static_cast<int32_t>(num_slots >> shift);
+    a.max_pages = static_cast<int32_t>(max_pages);
+    a.page_shift = shift;
+    a.B = static_cast<int32_t>(B);
+    a.q_heads = static_cast<int32_t>(q_heads);
+    a.kv_heads = static_cast<int32_t>(kv_heads);
+    a.group = static_cast<int32_t>(q_heads / kv_heads);
+    a.max_q = static_cast<int32_t>(std::min(max_q_len, T));
+    a.causal = causal != 0;
+    a.scale = scale;
+    return launch_attention(*d, a, workspace, static_cast<cudaStream_t>(stream));
 }
 
 fp8bq_status fp8bq_nvfp4_quantize_weight(const void *w_bf16, int64_t N, int64_t K, uint8_t *packed,

@@ -1,0 +1,148 @@
+// rms_norm.cuh -- root-mean-square norm with the residual's addition, quantized
+// for the FP8 linear layer that follows.
+//
+//     r = BF16(x + residual)                     (r = x without a residual)
+//     h = r * (mean(r^2) + eps)^(-1/2) * w       (FP32)
+//     s[g] = amax(|h| over 128 channels) / 448, or 1;  q = E4M3(h / s)
+// r is rounded to BF16 before the norm because that is the residual stream the
+// next layer reads; h itself is never rounded before its quantization (a BF16
+// h would round every value twice), only its optional BF16 copy is.
+//
+// HBM-bound: 2 bytes of x and 2 of the residual read, 2 of the residual and
+// 1 + 1/32 of codes and scales written per element.  One CTA holds one row in
+// registers (V vectors of 8 channels per thread, thread t has vectors t, t + n,
+// ...), so every byte moves once; 16 consecutive lanes hold the 128 channels of
+// one scale.  CTAs stride over the rows and keep the weight in registers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "ptx.cuh"
+#include "quantize.cuh"
+
+namespace fp8bq {
+
+constexpr int kNormMaxThreads = 1024;
+
+// Two floats -> packed BF16 (round to nearest even), `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void unpack_bf16x8(uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
+    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                      pack_bf16(f[6], f[7]));
+}
+
+// residual may be null (r = x); residual_out may be the same buffer as residual
+// or x (a thread reads its vectors before it writes them).  q and s are both
+// null or both given; h may be null.
+template <int V>
+__global__ void __launch_bounds__(kNormMaxThreads)
+rms_norm_kernel(const uint4 *x, const uint4 *residual, const uint4 *__restrict__ weight, float eps,
+                int64_t M, int nvec, uint4 *residual_out, uint2 *__restrict__ q,
+                float *__restrict__ s, uint4 *__restrict__ h) {
+    __shared__ float warp_sum[2][kNormMaxThreads / 32];
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int n = blockDim.x, warps = n >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float inv_k = 1.0f / static_cast<float>(nvec * 8);
+    uint4 w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * n;
+        w[i] = c < nvec ? __ldg(weight + c) : make_uint4(0, 0, 0, 0);
+    }
+    int buf = 0;
+    for (int64_t row = blockIdx.x; row < M; row += gridDim.x, buf ^= 1) {
+        const int64_t base = row * nvec;
+        uint4 v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = threadIdx.x + i * n;
+            v[i] = c < nvec ? x[base + c] : make_uint4(0, 0, 0, 0);
+        }
+        if (residual != nullptr) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = threadIdx.x + i * n;
+                if (c < nvec) {
+                    float a[8], b[8];
+                    unpack_bf16x8(v[i], a);
+                    unpack_bf16x8(residual[base + c], b);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) a[j] += b[j];
+                    v[i] = pack_bf16x8(a);
+                    residual_out[base + c] = v[i];
+                }
+            }
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float a[8];
+            unpack_bf16x8(v[i], a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fmaf(a[j], a[j], sum);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        // two buffers: a warp may be one row ahead of the slowest reader
+        if (lane == 0) warp_sum[buf][warp] = sum;
+        __syncthreads();
+        sum = lane < warps ? warp_sum[buf][lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float inv = rsqrtf(fmaf(sum, inv_k, eps));
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = threadIdx.x + i * n;
+            float a[8], g[8];
+            unpack_bf16x8(v[i], a);
+            unpack_bf16x8(w[i], g);
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[j] = a[j] * inv * g[j];
+                top = fmaxf(top, fabsf(a[j]));
+            }
+            if (h != nullptr && c < nvec) h[base + c] = pack_bf16x8(a);
+            if (q == nullptr) continue;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            if (c < nvec) {
+                const float scale = top == 0.0f ? 1.0f : __fdiv_rn(top, 448.0f);
+                uint32_t e[4];
+                if (scale >= kCorrectedQuotientMinScale) {
+                    const float y = __frcp_rn(scale);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        e[j] = e4m3x2_satfinite(corrected_quotient(a[2 * j], scale, y),
+                                                corrected_quotient(a[2 * j + 1], scale, y));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        e[j] = e4m3x2_satfinite(__fdiv_rn(a[2 * j], scale),
+                                                __fdiv_rn(a[2 * j + 1], scale));
+                }
+                q[base + c] = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+                if ((lane & 15) == 0) s[(base + c) >> 4] = scale;
+            }
+        }
+    }
+}
+
+}  // namespace fp8bq

@@ -77,7 +77,7 @@ typedef enum {
     FP8BQ_ERR_CUDA = 5,              /* a CUDA runtime or driver call failed */
     FP8BQ_ERR_TIMEOUT = 6,           /* a kernel abandoned a bounded wait */
     FP8BQ_ERR_NO_DEVICE = 7,         /* no sm_100 device is current */
-    FP8BQ_ERR_INDEX = 8              /* device side: a row's slot index was out of range */
+    FP8BQ_ERR_INDEX = 8              /* device side: a slot, page or length was out of range */
 } fp8bq_status;
 
 /* Operation selector for fp8bq_workspace_size. */
@@ -221,6 +221,136 @@ FP8BQ_API fp8bq_status fp8bq_gemm_silu_mul_quantize(const uint8_t *qa, const flo
                                                     int64_t I, int64_t K, uint8_t *q_e4m3,
                                                     float *s, void *h_bf16, void *workspace,
                                                     size_t ws_bytes, void *stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, quantized for the linear
+ * layer that follows (page "ProCreations/Nanbeige4.3-33B-DFlash2",
+ * "Architecture and checkpoint format": RMSNorm; page
+ * "ProCreations/Nanbeige4.3-33B-FP8", introduction: every linear layer's input
+ * is quantized per token and 128-channel group).  For every row:
+ *     r = BF16(x + residual)            (r = x when residual is NULL)
+ *     h = r * (mean(r^2) + eps)^(-1/2) * weight     in FP32
+ *     s[g] = amax(|h[128g : 128g+128]|) / 448, or 1 when that is 0
+ *     q = E4M3(h / s)                   nearest, ties to even, saturating
+ * The codes come from the FP32 h, not from its BF16 copy.
+ *   x_bf16            : in, BF16 [M, K]
+ *   residual_bf16     : in, BF16 [M, K], or NULL
+ *   weight_bf16       : in, BF16 [K]
+ *   residual_out_bf16 : out, BF16 [M, K], r; given exactly when residual_bf16
+ *                       is; may be the same buffer as residual_bf16 or x_bf16
+ *   q_e4m3, s         : out, codes [M, K] and scales [M, K/128]; both or neither
+ *   h_bf16            : out, optional BF16 [M, K], BF16(h); required without q_e4m3
+ * K a multiple of 128, at most 32768; eps >= 0 and finite.  Other than the
+ * aliasing named above, buffers must not overlap.
+ */
+FP8BQ_API fp8bq_status fp8bq_rms_norm_quantize(const void *x_bf16, const void *residual_bf16,
+                                               const void *weight_bf16, float eps, int64_t M,
+                                               int64_t K, void *residual_out_bf16,
+                                               uint8_t *q_e4m3, float *s, void *h_bf16,
+                                               void *stream);
+
+/* How the rotary frequencies are stretched for contexts longer than trained. */
+typedef enum {
+    FP8BQ_ROPE_PLAIN = 0,  /* f_i = base^(-2i/rot_dim) */
+    FP8BQ_ROPE_LINEAR = 1, /* f_i / factor (positions interpolated) */
+    FP8BQ_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) */
+    FP8BQ_ROPE_YARN = 3    /* f_i / factor for pairs that turn at most beta_slow times in
+                              old_context, f_i for those that turn beta_fast times or more,
+                              linear in the logarithm of the turns between; cos and sin times
+                              0.1 ln(factor) + 1 */
+} fp8bq_rope_scaling;
+
+/*
+ * Host helper: fills inv_freq[rot_dim / 2] (host memory) with the FP32 rotary
+ * frequencies and *mscale with the factor on cosine and sine.  factor >= 1 is
+ * used by every scaling but PLAIN; old_context, beta_fast > beta_slow > 0 by
+ * YARN only.  A user with another schedule fills the table itself.
+ */
+FP8BQ_API fp8bq_status fp8bq_rope_inv_freq(int64_t rot_dim, double base, fp8bq_rope_scaling scaling,
+                                           double factor, double old_context, double beta_fast,
+                                           double beta_slow, float *inv_freq, float *mscale);
+
+/*
+ * Rotary positions of the fused QKV output, keys and values written to the
+ * E4M3 cache (pages "ProCreations/Nanbeige4.3-33B-DFlash2", "Architecture and
+ * checkpoint format": rotary positions, base 1.2e8; "ProCreations/
+ * Nanbeige4.3-33B-FP8", "Serving": fp8_e4m3 cache with unit scales).  With
+ * u = positions[t] * inv_freq[j] (the exact product) and for pair j of each
+ * query and key head's first rot_dim channels
+ *     (a, b) -> mscale * (a cos u - b sin u, b cos u + a sin u),
+ * where (a, b) are channels (j, j + rot_dim/2), or (2j, 2j + 1) when
+ * interleaved is not 0; channels from rot_dim on pass unchanged.  Queries are
+ * rounded to BF16; keys are rounded once, to E4M3 (saturating), into slot
+ * loc[t] of k_cache; values go to v_cache as fp8bq_kv_write_e4m3 writes them.
+ *   qkv_bf16   : in, BF16 rows at (element) stride row_stride, columns
+ *                [q_heads | kv_heads | kv_heads] x head_dim
+ *   positions  : in, int64 [T];  loc : in, int64 [T] cache slots
+ *   inv_freq   : in, FP32 [rot_dim / 2], device memory
+ *   q_out_bf16 : out, BF16 rows at stride q_stride, [q_heads x head_dim]; may be
+ *                qkv_bf16 itself (then q_stride == row_stride), else no overlap
+ *   k_cache, v_cache, num_slots, slot_stride : as in fp8bq_kv_write_e4m3
+ * head_dim a multiple of 16 up to 256, rot_dim a multiple of 16 up to
+ * head_dim, strides multiples of 8 (slot_stride of 16), at most 1024 heads of
+ * each kind; qkv, q_out and the caches 16-byte, positions and loc 8-byte
+ * aligned.  A token with loc -1 is padding: nothing of it is written.  Any
+ * other slot outside [0, num_slots) skips the token too and is reported as
+ * FP8BQ_ERR_INDEX through fp8bq_last_device_status.
+ */
+FP8BQ_API fp8bq_status fp8bq_rope_kv_write_e4m3(
+    const void *qkv_bf16, int64_t row_stride, int64_t T, int64_t q_heads, int64_t kv_heads,
+    int64_t head_dim, const int64_t *positions, const float *inv_freq, int64_t rot_dim,
+    int interleaved, float mscale, const int64_t *loc, void *q_out_bf16, int64_t q_stride,
+    uint8_t *k_cache, uint8_t *v_cache, int64_t num_slots, int64_t slot_stride, void *stream);
+
+/*
+ * Attention of new tokens over the paged E4M3 cache (unit scales), for one
+ * token per sequence (decode), a few (a drafter's block) or many (a prefill
+ * chunk), mixed in one batch.  Page "ProCreations/Nanbeige4.3-33B-FP8",
+ * "Serving": chunked prefill and decode over an fp8_e4m3 cache.
+ * Sequence b has new tokens cu_q[b] .. cu_q[b+1] - 1 (rows of q and out) and
+ * seq_lens[b] cache positions, the new tokens' own among them (already
+ * written, e.g. by fp8bq_rope_kv_write_e4m3).  Position c lives in slot
+ * page_table[b, c / page_size] * page_size + c % page_size.  New token i sees
+ * positions 0 .. seq_lens[b] - q_len + i (causal != 0) or all seq_lens[b].
+ * For query head h and kv head h / (q_heads / kv_heads):
+ *     z_c = scale * (q . k_c),  lse = log sum_c exp(z_c),
+ *     out = BF16( sum_c exp(z_c - lse) v_c ).
+ * A token that sees no position gives zeros and lse = -infinity.
+ *   q_bf16, out_bf16 : BF16 rows at (element) strides q_stride, out_stride,
+ *                      [q_heads x 128]; must not overlap
+ *   k_cache, v_cache : in, E4M3 codes, slot s at byte offset s * slot_stride,
+ *                      [kv_heads x 128] (the layout fp8bq_kv_write_e4m3 writes)
+ *   page_table       : in, int32 [B, max_pages] at stride table_stride;
+ *                      entries beyond a sequence's length are not read
+ *   seq_lens [B], cu_q [B + 1] : in, int32, device memory, cu_q ascending from 0
+ *   max_q_len        : the most new tokens of any sequence
+ *   lse              : out, optional FP32 [T, q_heads]
+ *   workspace        : at least fp8bq_paged_attention_workspace_size(T, B, q_heads,
+ *                      kv_heads, max_q_len) bytes, same state rule as fp8bq_gemm
+ *                      (one workspace may serve both, in stream order)
+ * Heads have 128 channels; q_heads a multiple of kv_heads, at most 1024;
+ * page_size a power of two from 8 to 2^20, max_pages * page_size <= 2^30;
+ * B <= 65536, T < 2^21; scale > 0; q, out and the caches 16-byte aligned,
+ * q_stride and out_stride multiples of 8, slot_stride of 16.
+ * Slots at or behind a sequence's length may hold anything, NaN codes too;
+ * the cache positions that a sequence has must hold finite values, and q too.
+ * Rows of q and out at or behind cu_q[B] are padding: neither read nor written.
+ * What the host cannot see is checked on the device, without a fault, and
+ * reported as FP8BQ_ERR_INDEX through fp8bq_last_device_status: a page outside
+ * the cache (its positions read as zeros), a length that is negative or beyond
+ * max_pages * page_size (clamped), new tokens beyond max_q_len or T (skipped).
+ */
+FP8BQ_API fp8bq_status fp8bq_paged_attention(
+    const void *q_bf16, int64_t q_stride, const uint8_t *k_cache, const uint8_t *v_cache,
+    int64_t num_slots, int64_t slot_stride, const int32_t *page_table, int64_t table_stride,
+    int64_t max_pages, int64_t page_size, const int32_t *seq_lens, const int32_t *cu_q, int64_t B,
+    int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_q_len, float scale, int causal,
+    void *out_bf16, int64_t out_stride, float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace fp8bq_paged_attention requires (0 when none, and for
+ * arguments it would reject).  Always a multiple of 256. */
+FP8BQ_API size_t fp8bq_paged_attention_workspace_size(int64_t T, int64_t B, int64_t q_heads,
+                                                      int64_t kv_heads, int64_t max_q_len);
 
 /*
  * NVFP4 weight-only format with BF16 activations (page
