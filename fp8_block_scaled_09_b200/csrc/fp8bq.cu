@@ -42,6 +42,7 @@
 #include <utility>
 
 #include "attention.cuh"
+#include "attention_few.cuh"
 #include "fp8bq.h"
 #include "gemm_decode.cuh"
 #include "gemm_prefill.cuh"
@@ -243,6 +244,13 @@ const DeviceInfo *device_info() {
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  nvfp4::GemvLayout<2>::kBytes) != cudaSuccess)
             return;
+        if (cudaFuncSetAttribute(attn::attention_few_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 attn::Few<16>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(attn::attention_few_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 attn::Few<32>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(attn::attention_few_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 attn::Few<64>::kBytes) != cudaSuccess)
+            return;
         for (int c = 2; c <= 8; ++c) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(c));
@@ -334,11 +342,11 @@ struct TmapKey {
     uintptr_t ptr;
     int64_t rows, cols;
     uint32_t box_cols, box_rows;
-    int type, elem_bytes, swizzle;
+    int type, elem_bytes, swizzle, promotion;
     bool operator==(const TmapKey &o) const {
         return ptr == o.ptr && rows == o.rows && cols == o.cols && box_cols == o.box_cols &&
                box_rows == o.box_rows && type == o.type && elem_bytes == o.elem_bytes &&
-               swizzle == o.swizzle;
+               swizzle == o.swizzle && promotion == o.promotion;
     }
 };
 struct TmapKeyHash {
@@ -348,7 +356,8 @@ struct TmapKeyHash {
                                    (static_cast<uint64_t>(k.box_cols) << 32) | k.box_rows,
                                    (static_cast<uint64_t>(k.type) << 16) |
                                        static_cast<uint64_t>(k.elem_bytes),
-                                   static_cast<uint64_t>(k.swizzle)};
+                                   (static_cast<uint64_t>(k.promotion) << 8) |
+                                       static_cast<uint64_t>(k.swizzle)};
         for (uint64_t p : parts) h = (h ^ p) * 0x100000001B3ull;
         return static_cast<size_t>(h ^ (h >> 29));
     }
@@ -361,9 +370,11 @@ std::unordered_map<TmapKey, CUtensorMap, TmapKeyHash> g_tmap_cache;
 // box [box_rows, box_cols], zero fill out of bounds.
 bool make_tmap_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType type, int elem_bytes,
                   int64_t rows, int64_t cols, uint32_t box_cols, uint32_t box_rows,
-                  CUtensorMapSwizzle swizzle) {
+                  CUtensorMapSwizzle swizzle,
+                  CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     const TmapKey key{reinterpret_cast<uintptr_t>(ptr), rows, cols, box_cols, box_rows,
-                      static_cast<int>(type), elem_bytes, static_cast<int>(swizzle)};
+                      static_cast<int>(type), elem_bytes, static_cast<int>(swizzle),
+                      static_cast<int>(promotion)};
     {
         std::lock_guard<std::mutex> lk(g_tmap_mu);
         auto it = g_tmap_cache.find(key);
@@ -380,8 +391,7 @@ bool make_tmap_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType type, i
     const cuuint32_t elem[2] = {1u, 1u};
     std::memset(map, 0, sizeof(*map));
     if (enc(map, type, 2, const_cast<void *>(ptr), dims, strides, box, elem,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
     std::lock_guard<std::mutex> lk(g_tmap_mu);
     if (g_tmap_cache.size() >= kTmapCacheMax) g_tmap_cache.clear();
@@ -703,9 +713,52 @@ fp8bq_status check_attention(int64_t T, int64_t B, int64_t q_heads, int64_t kv_h
     return FP8BQ_OK;
 }
 
-size_t attention_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+// Query rows of one kv head that the largest sequence has.
+int64_t attention_rows(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_q_len) {
+    return std::min(max_q_len, T) * (q_heads / kv_heads);
+}
 
-fp8bq_status launch_attention(const DeviceInfo &d, const attn::Args &a, void *, cudaStream_t st) {
+template <int N>
+size_t few_ws_bytes() {
+    return round256(decode::kCounterBytes + int64_t(2) * decode::kMaxGrid * attn::Few<N>::kPartial * 4);
+}
+
+size_t attention_ws_bytes(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_q_len) {
+    const int64_t rows = attention_rows(T, q_heads, kv_heads, max_q_len);
+    return rows <= 16 ? few_ws_bytes<16>() : rows <= 32 ? few_ws_bytes<32>() : rows <= 64 ? few_ws_bytes<64>() : 0;
+}
+
+template <int N>
+cudaError_t launch_few(const DeviceInfo &d, const attn::Args &a, const CUtensorMap &tk,
+                       const CUtensorMap &tv, void *ws, cudaStream_t st) {
+    const int grid = std::min<int>(d.sm_count, decode::kMaxGrid);
+    return launch(attn::attention_few_kernel<N>, dim3(static_cast<unsigned>(grid)),
+                  dim3(attn::kFewThreads), attn::Few<N>::kBytes, st, tk, tv, a,
+                  static_cast<int *>(ws),
+                  reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + decode::kCounterBytes),
+                  d.status);
+}
+
+fp8bq_status launch_attention(const DeviceInfo &d, const attn::Args &a, int64_t num_slots, void *ws,
+                              cudaStream_t st) {
+    const int64_t rows = int64_t(a.max_q) * a.group;
+    if (rows <= 64) {
+        // without a slot there is nothing to map: any descriptor will do, no
+        // page is in the cache
+        CUtensorMap tk, tv;
+        const uint32_t box = std::min<uint32_t>(1u << a.page_shift, attn::kTile);
+        const void *k = num_slots ? static_cast<const void *>(a.k_cache) : ws;
+        const void *v = num_slots ? static_cast<const void *>(a.v_cache) : ws;
+        const int64_t slots = std::max<int64_t>(num_slots, 1);
+        if (!make_tmap_2d(&tk, k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, slots, a.slot_stride, attn::kDim,
+                          box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
+            !make_tmap_2d(&tv, v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, slots, a.slot_stride, attn::kDim,
+                          box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
+            return FP8BQ_ERR_CUDA;
+        return from_cuda(rows <= 16   ? launch_few<16>(d, a, tk, tv, ws, st)
+                         : rows <= 32 ? launch_few<32>(d, a, tk, tv, ws, st)
+                                      : launch_few<64>(d, a, tk, tv, ws, st));
+    }
     return from_cuda(launch(attn::attention_simple_kernel,
                             dim3(static_cast<unsigned>(a.T * a.q_heads)),
                             dim3(32 * attn::kSimpleWarps), 0, st, a, d.status));
@@ -955,7 +1008,7 @@ fp8bq_status fp8bq_rope_kv_write_e4m3(const void *qkv_bf16, int64_t row_stride, 
 size_t fp8bq_paged_attention_workspace_size(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads,
                                             int64_t max_q_len) {
     if (check_attention(T, B, q_heads, kv_heads, max_q_len) != FP8BQ_OK || T == 0) return 0;
-    return attention_ws_bytes(T, B, q_heads, kv_heads, max_q_len);
+    return attention_ws_bytes(T, q_heads, kv_heads, max_q_len);
 }
 
 fp8bq_status fp8bq_paged_attention(const void *q_bf16, int64_t q_stride, const uint8_t *k_cache,
@@ -992,7 +1045,7 @@ fp8bq_status fp8bq_paged_attention(const void *q_bf16, int64_t q_stride, const u
         ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens) |
           reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(lse)) & 3u) != 0)
         return FP8BQ_ERR_MISALIGNED;
-    const size_t need = attention_ws_bytes(T, B, q_heads, kv_heads, max_q_len);
+    const size_t need = attention_ws_bytes(T, q_heads, kv_heads, max_q_len);
     if (need && (!workspace || ws_bytes < need)) return FP8BQ_ERR_WORKSPACE;
     if (need && !aligned16(workspace)) return FP8BQ_ERR_MISALIGNED;
     const DeviceInfo *d = device_info();
@@ -1021,7 +1074,7 @@ fp8bq_status fp8bq_paged_attention(const void *q_bf16, int64_t q_stride, const u
     a.max_q = static_cast<int32_t>(std::min(max_q_len, T));
     a.causal = causal != 0;
     a.scale = scale;
-    return launch_attention(*d, a, workspace, static_cast<cudaStream_t>(stream));
+    return launch_attention(*d, a, num_slots, workspace, static_cast<cudaStream_t>(stream));
 }
 
 fp8bq_status fp8bq_nvfp4_quantize_weight(const void *w_bf16, int64_t N, int64_t K, uint8_t *packed,

@@ -41,17 +41,24 @@ def rope(x, positions, inv_freq, mscale, interleaved):
 
 
 def attention(q, k_cache, v_cache, table, seq_lens, cu_q, page, q_heads, kv_heads, scale, causal):
-    """(out, lse, bound) float64 [T, q_heads, 128], [T, q_heads] and the error bound of out.
+    """(out, lse, bound, lse_bound): float64 [T, q_heads, 128], [T, q_heads], and error bounds of both.
 
     The bound: half a BF16 step of the output, plus what the weights may be off by.  A weight
     is off by 2^-10 of itself (rounded to at least 11 bits, or to two E4M3 parts of 4 bits, and
     an exponential of a few FP32 ulps), by 2^-17 of the row's largest (the two-part rounding's
     absolute floor), and by twice the error of its exponent: q may be held in two E4M3 parts
-    (off by 2^-17 of its row's largest channel) and 128 products are summed in FP32."""
+    (off by 2^-17 of its row's largest channel) and 128 products are summed in FP32.
+
+    lse: every exponent is off by that dz at most, so log sum exp(z + e), |e| <= dz, is off by dz at
+    most (each term changes by a factor within exp(+-dz)).  dz is relative to the sum of the
+    products' sizes, not to the logit, which may cancel.  The weights' sum adds 2^-16 (exponentials
+    and additions, a few FP32 ulps each over at most 2^13 positions), the result's own FP32
+    arithmetic (maximum + logarithm, changes of base) 2^-21 of it."""
     q = q.cpu().double().view(q.shape[0], q_heads, 128)
     kc, vc = (e4m3_values(c)[:, :kv_heads * 128].view(-1, kv_heads, 128) for c in (k_cache, v_cache))
     table, lens, cu = table.cpu().long(), seq_lens.cpu().tolist(), cu_q.cpu().tolist()
     out, bound = torch.zeros_like(q), torch.zeros_like(q)
+    lse_bound = torch.zeros(q.shape[:2], dtype=torch.float64)
     lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64)
     for b, n in enumerate(lens):
         rows = range(cu[b], cu[b + 1])
@@ -74,11 +81,12 @@ def attention(q, k_cache, v_cache, table, seq_lens, cu_q, page, q_heads, kv_head
                 o = w @ v
                 dz = scale * (2.0 ** -17 * x.abs().amax(1) * k.abs().sum(1).max() +
                               128 * 2.0 ** -23 * (x.abs() @ k.abs().T).amax(1))
+                lse_bound[cu[b]:cu[b + 1], h] = dz + 2.0 ** -16 + 2.0 ** -21 * torch.where(torch.isinf(l), 0.0, l.abs())
                 off = (w * (2.0 ** -10 + 2 * dz[:, None])) @ v.abs()
                 off += 2.0 ** -17 * w.amax(1, keepdim=True) * ((w > 0).double() @ v.abs())
                 out[cu[b]:cu[b + 1], h] = o
                 bound[cu[b]:cu[b + 1], h] = HALF_BF16 * o.abs() + off + 1e-30
-    return out, lse, bound
+    return out, lse, bound, lse_bound
 
 
 def random_batch(q_lens, ctx, q_heads, kv_heads, page, seed, slot_pad=0, spare_pages=3, stale=0x7F):
