@@ -1,36 +1,40 @@
 // attention_few.cuh -- paged attention for few query rows per kv head (decode,
-// a drafter's block): q_len * group <= N rows, N = 16, 32 or 64.
+// a short block): q_len * group <= NR rows, NR = 8, 16 or 32.
 //
 // Bound by the cache's bytes: 256 per position and kv head, read once.  The
 // E4M3 codes go from HBM to shared memory by TMA and from there straight into
 // the tensor cores, with the roles of rows and columns swapped: 128 cache
 // positions are the MMA's M, the query rows its N.
-//     S^T[pos, row] = K[pos, :] . Q[row, :]       M = 128, N rows, K = 128
-//     O^T[ch, row] += V[:, ch]^T . P[:, row]      M = 128, N rows, K = 128 positions
+//     S^T[pos, row] = K[pos, :] . Q[row, :]       M = 128, N = 2 NR, K = 128
+//     O^T[ch, row] += V[:, ch]^T . P[:, row]      M = 128, N = 2 NR, K = 128 positions
 // Neither K nor V is ever converted: V is the A operand with its channels
 // contiguous.  Queries and weights keep their precision as two E4M3 parts,
-// x = hi + lo (two MMAs into one accumulator): hi holds 4 significant bits, lo
-// the next 4, so a BF16 query is exact down to 2^-9 of its row's largest
-// channel (rows are scaled by a power of two to [128, 256)), and a weight p
-// (scaled by 256) has 8 bits down to 2^-10 of the largest and an absolute
-// error of 2^-18 below.  At N = 16 the two MMAs per tile take a small part of
-// the time that a 16 KB tile needs to arrive (0.37 us per SM at 6.5 TB/s).
+// x = hi + lo, in two columns whose results are added: hi holds 4 significant
+// bits, lo the next 4, so a BF16 query is exact down to 2^-9 of its row's
+// largest channel (rows are scaled by a power of two to [128, 256)), and a
+// weight p (scaled by 256) has 8 bits down to 2^-10 of the largest and an
+// absolute error of 2^-18 below.  (Two MMAs into one column cost more: an MMA
+// with this few columns takes the time to read its 4 KB of A, and with twice
+// as many of them the tensor pipe was busy 1100 of 2550 cycles per tile.)
 //
 // Work is a list of tiles of 128 positions, ordered by (sequence, kv head,
-// tile); CTA c of a grid of one CTA per SM takes the c-th equal part, whatever
-// the sequences' lengths.  A part's tiles of one (sequence, head), its segment,
-// are taken in chunks of at most kChunk tiles, as many as TMEM holds scores
-// for (twice): a chunk's scores are all there before its softmax, so no output
-// is ever rescaled in TMEM; the chunk's O^T is merged into registers with the
-// usual factor exp(m_old - m_new).  The ring carries K of chunk g + 1 ahead of V of
-// chunk g, so the next scores are computed while the softmax works.
-// A (sequence, head) that lies in several CTAs leaves FP32 partials and
-// maxima in the workspace; the last CTA to arrive (a counter) joins them in
-// the order of the CTAs, so results do not depend on timing.
+// tile), each head preceded by kHeadCost tiles' worth of nothing for what
+// beginning and ending it costs; CTA c of a grid of one CTA per SM takes the
+// c-th equal part, whatever the sequences' lengths.  A part's tiles of one
+// (sequence, head), its segment, are taken in chunks of at most kChunk tiles,
+// as many as TMEM holds scores for (twice): a chunk's scores are all there
+// before its softmax, so no output is ever rescaled in TMEM; the chunk's O^T is
+// merged into registers with the usual factor exp(m_old - m_new), one chunk
+// later, so that nothing waits for its MMAs.  The ring carries K of chunk
+// g + 1 ahead of V of chunk g, so the next scores are computed while the
+// softmax works.  A (sequence, head) that lies in several CTAs leaves FP32
+// partials and maxima in the workspace; the last CTA to arrive (a counter)
+// joins them in the order of the CTAs, so results do not depend on timing.
 //
-// Roles: warp 0 TMA producer (a page per lane), warp 1 MMA issuer, warps 2..5
-// softmax: thread = one position of the tile (its TMEM lane) in the score
-// phase, one output channel in the merge.
+// Roles: warp 0 TMA producer (a page per lane), warp 1 MMA issuer, warps 2..9
+// softmax (two groups of four that take a chunk's tiles in turn; thread = one
+// position of the tile, its TMEM lane, in the score phase, one output channel
+// of half the rows in the merge), warp 10 queries.
 #pragma once
 
 #include "attention.cuh"
@@ -42,34 +46,85 @@ namespace attn {
 
 constexpr int kTile = 128;                 // positions
 constexpr int kStageBytes = kTile * kDim;  // one K or V tile of codes
-constexpr int kFewThreads = 192;
-constexpr float kPScale = 8.0f;            // weights are held times 2^8
+constexpr int kFewSoftmaxWarps = 8;
+constexpr int kFewThreads = 32 * (3 + kFewSoftmaxWarps);
+constexpr int kHeadCost = 2;     // tiles' worth of work that a (sequence, head) adds
+constexpr float kPScale = 8.0f;  // weights are held times 2^8
 
-template <int N>
+template <int NR>
 struct Few {
-    static constexpr int kChunk = 256 / N - 1;  // tiles; 2 chunks + 2 outputs = 512 columns
-    static constexpr int kQ = N * kDim;         // bytes of one part of Q
-    static constexpr int kP = N * kTile;        // bytes of one part of P
-    static constexpr int kPSlots = N == 64 ? 2 : 4;
-    static constexpr int kStages = N == 64 ? 9 : N == 32 ? 10 : 12;
-    static constexpr int kQOff = kStages * kStageBytes;          // [2 buffers][hi, lo]
-    static constexpr int kPOff = kQOff + 2 * 2 * kQ;             // [kPSlots][hi, lo]
-    static constexpr int kBarOff = kPOff + kPSlots * 2 * kP;
-    // full, empty; pfull, pempty; qfull, sfull, sfree, ofull, ofree (two each); vready
-    static constexpr int kBars = 2 * kStages + 2 * kPSlots + 11;
-    static constexpr int kRowOff = kBarOff + kBars * 8;  // per-row values
-    static constexpr int kBytes = kRowOff + (2 + 2 + 4 + 1 + 1 + 4 + 2) * N * 4 + 64 + 1024;
+    static constexpr int kN = 2 * NR;            // MMA columns: hi and lo parts
+    static constexpr int kChunk = 256 / kN - 1;  // tiles; 2 chunks + 2 outputs = 512 columns
+    static constexpr int kQ = kN * kDim;         // bytes of Q
+    static constexpr int kP = kN * kTile;        // bytes of P
+    // a whole chunk of P, so that the softmax never waits for V; half per group
+    static constexpr int kGroupSlots = (kChunk + 1) / 2;
+    static constexpr int kPSlots = 2 * kGroupSlots;
+    static constexpr int kStages = NR == 32 ? 10 : 11;
+    static constexpr int kQOff = kStages * kStageBytes;  // [2]
+    static constexpr int kPOff = kQOff + 2 * kQ;         // [kPSlots]
+    static constexpr int kBarOff = kPOff + kPSlots * kP;
+    // full, empty; pfull, pempty; qfull (4), qempty, sfull, sfree, ofull, ofree, vready (2 each)
+    static constexpr int kBars = 2 * kStages + 2 * kPSlots + 4 + 12;
+    // per-row values: scale and limit [4], maximum and factor [2], negated maximum,
+    // reductions over the warps [8], sums over the warps [2][8]
+    static constexpr int kRowOff = kBarOff + kBars * 8;
+    static constexpr int kBytes = kRowOff + (4 + 4 + 2 + 2 + 1 + 8 + 16) * NR * 4 + 64 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory");
-    static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kQ % 1024 == 0 && kP % 1024 == 0,
-                  "swizzled tiles");
-    static constexpr int kPartial = N * (kDim + 2);  // floats: O [N][128], max [N], sum [N]
-    __device__ static uint32_t s_col(int buf, int j) { return (buf * kChunk + j) * N; }
-    __device__ static uint32_t o_col(int buf) { return (2 * kChunk + buf) * N; }
+    static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kQ % 1024 == 0, "swizzled tiles");
+    static constexpr int kPartial = NR * (kDim + 2);  // floats: O [NR][128], max [NR], sum [NR]
+    __device__ static uint32_t s_col(int buf, int j) { return (buf * kChunk + j) * kN; }
+    __device__ static uint32_t o_col(int buf) { return (2 * kChunk + buf) * kN; }
 };
 
-// idesc of E4M3 x E4M3 with the A operand's M dimension contiguous
-__host__ __device__ constexpr uint32_t idesc_e4m3_a_mn(int m, int n) {
-    return umma_idesc_e4m3(m, n) | (1u << 15);
+// idesc of E4M3 x E4M3 with the M dimension of A and the N dimension of B contiguous
+__host__ __device__ constexpr uint32_t idesc_e4m3_mn(int m, int n) {
+    return umma_idesc_e4m3(m, n) | (1u << 15) | (1u << 16);
+}
+
+// Unswizzled operand tile whose M or N dimension is contiguous: blocks of 16
+// bytes of it by 8 K rows (128 bytes); `k_step` bytes between blocks along K,
+// `mn_step` along M or N.
+__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t mn_step, uint32_t k_step) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(k_step >> 4) << 16;
+    d |= static_cast<uint64_t>(mn_step >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;  // descriptor version for sm_100
+    return d;
+}
+
+// X consecutive TMEM columns of this warp's lanes, without the wait.
+template <int X>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float *v) {
+    static_assert(X == 4 || X == 8 || X == 16, "columns");
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    if constexpr (X == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+    else if constexpr (X == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+}
+
+// Waits for this warp's TMEM loads into v[0, X); the values pass through the
+// statement, so that no use of them moves before it.
+template <int X>
+__device__ __forceinline__ void tmem_ld_wait(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < X; ++i) asm volatile("" : "+f"(v[i]));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -135,11 +190,16 @@ __device__ __forceinline__ int page_row(const Args &a, int b, int idx, int len, 
     return page << a.page_shift;
 }
 
-// The chunks of one CTA's part of the tile list, in order.
-template <int N>
+// Positions of the work list that one head of a sequence takes.
+__device__ __forceinline__ int64_t head_cost(int tiles) {
+    return tiles > 0 ? static_cast<int64_t>(tiles) + kHeadCost : 0;
+}
+
+// The chunks of one CTA's part of the work list, in order.
+template <int NR>
 struct Chunks {
     const Args &a;
-    int64_t w, w_end, base;  // next tile, end of the part, first tile of sequence b
+    int64_t w, w_end, base;  // next position, end of the part, first position of sequence b
     int b, tiles;            // sequence of w, its tiles per head
     Seq seq;
     // the current chunk
@@ -148,8 +208,8 @@ struct Chunks {
     bool first, last;        // of its segment
 
     __device__ Chunks(const Args &args, int64_t w0, int64_t w1, int b0, int64_t base0)
-        : a(args), w(w0), w_end(w1), base(base0), b(b0), tiles(0), seg_end(0) {
-        t = n = 0;
+        : a(args), w(w0), w_end(w1), base(base0), b(b0), tiles(0), hk(0), t(0), n(0), seg_t0(0),
+          seg_end(0), first(false), last(false) {
         if (w < w_end) {
             seq = seq_of(a, b);
             tiles = seq_tiles(seq);
@@ -157,37 +217,41 @@ struct Chunks {
     }
     __device__ bool next() {
         t += n;
-        if (t >= seg_end) {  // a new segment
+        while (t >= seg_end) {  // a new segment
+            n = 0;
             if (w >= w_end) return false;
-            while (w >= base + static_cast<int64_t>(tiles) * a.kv_heads) {
-                base += static_cast<int64_t>(tiles) * a.kv_heads;
+            while (w >= base + head_cost(tiles) * a.kv_heads) {
+                base += head_cost(tiles) * a.kv_heads;
                 seq = seq_of(a, ++b);
                 tiles = seq_tiles(seq);
             }
-            const int rel = static_cast<int>(w - base);
-            hk = rel / tiles;
-            t = seg_t0 = rel - hk * tiles;
-            seg_end = static_cast<int>(min(static_cast<int64_t>(tiles), t + (w_end - w)));
-            w += seg_end - t;
+            const int cost = static_cast<int>(head_cost(tiles));
+            const int rel = static_cast<int>((w - base) % cost);
+            hk = static_cast<int>((w - base) / cost);
+            const int64_t left = min(static_cast<int64_t>(cost - rel), w_end - w);
+            t = seg_t0 = max(rel - kHeadCost, 0);
+            seg_end = max(static_cast<int>(rel + left) - kHeadCost, 0);
+            w += left;
         }
         first = t == seg_t0;
         // equal chunks, so that no segment ends in a short one
         const int total = seg_end - seg_t0;
-        const int parts = (total + Few<N>::kChunk - 1) / Few<N>::kChunk;
+        const int parts = (total + Few<NR>::kChunk - 1) / Few<NR>::kChunk;
         n = min((total + parts - 1) / parts, seg_end - t);
         last = t + n == seg_end;
         return true;
     }
-    // the list's first tile of the current (sequence, head)
-    __device__ int64_t item() const { return base + static_cast<int64_t>(hk) * tiles; }
+    // the list's position of the current (sequence, head)'s first tile
+    __device__ int64_t item() const { return base + hk * head_cost(tiles) + kHeadCost; }
 };
 
-template <int N>
+template <int NR>
 __global__ void __launch_bounds__(kFewThreads, 1)
 attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const Args a, int *counters,
                      float *partials, int *status) {
-    using F = Few<N>;
+    using F = Few<NR>;
+    constexpr int N = F::kN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -195,16 +259,16 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t *empty = full + F::kStages;
     uint64_t *pfull = empty + F::kStages;
     uint64_t *pempty = pfull + F::kPSlots;
-    uint64_t *qfull = pempty + F::kPSlots, *sfull = qfull + 2, *sfree = sfull + 2,
-             *ofull = sfree + 2, *ofree = ofull + 2, *vready = ofree + 2;
-    float *row_scale = reinterpret_cast<float *>(smem + F::kRowOff);  // [2][N] score -> log2 weight
-    float *row_max = row_scale + 2 * N;    // [2][N] running maximum (log2), by chunk parity
-    float *row_red = row_max + 2 * N;      // [4][N] per softmax warp
-    float *row_neg = row_red + 4 * N;      // [N] kPScale - maximum
-    float *row_fac = row_neg + N;          // [N] exp2(old maximum - new)
-    float *row_sum = row_fac + N;          // [4][N] sums per softmax warp
-    int *row_lim = reinterpret_cast<int *>(row_sum + 4 * N);  // [2][N] last position a row sees
-    uint32_t *misc = reinterpret_cast<uint32_t *>(row_lim + 2 * N);
+    uint64_t *qfull = pempty + F::kPSlots, *qempty = qfull + 4, *sfull = qempty + 2,
+             *sfree = sfull + 2, *ofull = sfree + 2, *ofree = ofull + 2, *vready = ofree + 2;
+    float *row_scale = reinterpret_cast<float *>(smem + F::kRowOff);  // [4] score -> log2 weight
+    int *row_lim = reinterpret_cast<int *>(row_scale + 4 * NR);       // [4] last position seen
+    float *row_max = reinterpret_cast<float *>(row_lim + 4 * NR);     // [2] maximum (log2), by chunk
+    float *row_fac = row_max + 2 * NR;   // [2] exp2(old maximum - new), by chunk
+    float *row_neg = row_fac + 2 * NR;   // kPScale - maximum
+    float *row_red = row_neg + NR;       // [8] maxima per softmax warp
+    float *row_sum = row_red + 8 * NR;   // [2][8] sums per softmax warp, by chunk
+    uint32_t *misc = reinterpret_cast<uint32_t *>(row_sum + 16 * NR);
     uint32_t *tmem_slot = misc;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     int *shared_last = reinterpret_cast<int *>(misc + 2);
@@ -223,14 +287,15 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(&pfull[i], 4);
             mbar_init(&pempty[i], 1);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&qfull[i], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&qfull[i], 4);
+            mbar_init(&qempty[i], 1);
             mbar_init(&sfull[i], 1);
-            mbar_init(&sfree[i], 4);
+            mbar_init(&sfree[i], kFewSoftmaxWarps);
             mbar_init(&ofull[i], 1);
-            mbar_init(&ofree[i], 4);
+            mbar_init(&ofree[i], kFewSoftmaxWarps);
+            mbar_init(&vready[i], 1);
         }
-        mbar_init(vready, 1);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tmap(&tmap_k);
@@ -242,11 +307,11 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     grid_dependency_wait();
     if (warp == 0) {
-        // this CTA's part of the tile list: lane l sums the tiles of the l-th
-        // run of sequences, then the lane whose run holds the first tile finds it
+        // this CTA's part of the work list: lane l sums the costs of the l-th
+        // run of sequences, then the lane whose run holds the first position finds it
         const int per = (a.B + 31) / 32, b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
         int64_t mine = 0;
-        for (int b = b0; b < b1; ++b) mine += seq_tiles(seq_of(a, b));
+        for (int b = b0; b < b1; ++b) mine += head_cost(seq_tiles(seq_of(a, b)));
         mine *= a.kv_heads;
         int64_t incl = mine;
 #pragma unroll
@@ -262,7 +327,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             int64_t base = incl - mine;
             int b = b0;
             for (;; ++b) {
-                const int64_t n = static_cast<int64_t>(seq_tiles(seq_of(a, b))) * a.kv_heads;
+                const int64_t n = head_cost(seq_tiles(seq_of(a, b))) * a.kv_heads;
                 if (w0 < base + n) break;
                 base += n;
             }
@@ -280,18 +345,18 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    Chunks<N> ahead(a, start_w[0], start_w[1], *start_b, start_w[2]);
-    Chunks<N> cur(a, start_w[0], start_w[1], *start_b, start_w[2]);
-    bool more = ahead.next();  // the chunk whose K comes next
+    Chunks<NR> cur(a, start_w[0], start_w[1], *start_b, start_w[2]);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
+        Chunks<NR> ahead = cur;  // the chunk whose K comes next
+        bool more = ahead.next();
         const uint64_t evict_first = l2_policy_evict_first();
         const int page = 1 << a.page_shift;
         const int rows = min(page, kTile), boxes = kTile / rows;
         uint32_t stage = 0, phase = 0, issued = 0;
         bool ok = true;
-        auto tiles = [&](const Chunks<N> &c, const CUtensorMap *map) {
+        auto tiles = [&](const Chunks<NR> &c, const CUtensorMap *map) {
             // the next tile's page while this one waits for its slot
             auto row_at = [&](int t) {
                 if (lane >= boxes || t >= c.t + c.n) return -kTile;
@@ -333,8 +398,11 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
-            const uint32_t id_s = umma_idesc_e4m3(kTile, N), id_o = idesc_e4m3_a_mn(kDim, N);
-            uint32_t stage = 0, phase = 0, pslot = 0, pphase = 0;
+            Chunks<NR> ahead = cur;
+            bool more = ahead.next();
+            const uint32_t id_s = umma_idesc_e4m3(kTile, N), id_o = idesc_e4m3_mn(kDim, N);
+            uint32_t stage = 0, phase = 0;
+            uint32_t pslot[2] = {0, 0}, pphase[2] = {0, 0};  // of each softmax group
             uint32_t gk = 0, gv = 0, segs = 0;  // chunks and segments so far
             bool ok = true;
             auto advance = [&] {
@@ -343,30 +411,30 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     phase ^= 1;
                 }
             };
-            auto scores = [&](const Chunks<N> &c) {
+            auto scores = [&](const Chunks<NR> &c) {
                 if (c.first) {
-                    ok = ok && mbar_wait(&qfull[segs & 1], (segs >> 1) & 1, abort_flag, status);
+                    ok = ok && mbar_wait(&qfull[segs & 3], (segs >> 2) & 1, abort_flag, status);
                     ++segs;
                 }
                 const uint32_t buf = gk & 1;
                 ok = ok && mbar_wait(&sfree[buf], ((gk >> 1) & 1) ^ 1, abort_flag, status);
-                const uint32_t q = smem_addr(smem + F::kQOff + ((segs - 1) & 1) * 2 * F::kQ);
+                const uint32_t q = smem_addr(smem + F::kQOff + ((segs - 1) & 1) * F::kQ);
                 for (int j = 0; j < c.n && ok; ++j) {
                     ok = mbar_wait(&full[stage], phase, abort_flag, status);
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t k = smem_addr(smem + stage * kStageBytes);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            umma_e4m3(tmem + F::s_col(buf, j), umma_desc_sw128(k + 32 * s),
-                                      umma_desc_sw128(q + part * F::kQ + 32 * s), id_s,
-                                      part + s > 0 ? 1u : 0u);
+                    for (int s = 0; s < 4; ++s)
+                        umma_e4m3(tmem + F::s_col(buf, j), umma_desc_sw128(k + 32 * s),
+                                  umma_desc_sw128(q + 32 * s), id_s, s > 0 ? 1u : 0u);
                     umma_commit(&empty[stage]);
                     advance();
                 }
-                if (ok) umma_commit(&sfull[buf]);
+                if (ok) {
+                    umma_commit(&sfull[buf]);
+                    if (c.last) umma_commit(&qempty[(segs - 1) & 1]);
+                }
                 ++gk;
             };
             if (more) scores(ahead);
@@ -376,39 +444,104 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const uint32_t buf = gv & 1;
                 ok = ok && mbar_wait(&ofree[buf], ((gv >> 1) & 1) ^ 1, abort_flag, status);
                 for (int j = 0; j < cur.n && ok; ++j) {
+                    const int h = j & 1;
+                    const uint32_t slot = h * F::kGroupSlots + pslot[h];
                     ok = mbar_wait(&full[stage], phase, abort_flag, status);
-                    // the sequence ends in this tile: the softmax warps clear what is behind
-                    if (ok && (cur.t + j + 1) * kTile > cur.seq.len) mbar_arrive(vready);
-                    ok = ok && mbar_wait(&pfull[pslot], pphase, abort_flag, status);
+                    // the sequence ends in this tile: its softmax group clears what is behind
+                    if (ok && (cur.t + j + 1) * kTile > cur.seq.len) mbar_arrive(&vready[h]);
+                    ok = ok && mbar_wait(&pfull[slot], pphase[h], abort_flag, status);
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t v = smem_addr(smem + stage * kStageBytes);
-                    const uint32_t p = smem_addr(smem + F::kPOff + pslot * 2 * F::kP);
+                    const uint32_t p = smem_addr(smem + F::kPOff + slot * F::kP);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)  // 32 positions each
-                            umma_e4m3(tmem + F::o_col(buf), umma_desc_sw128(v + 32 * kDim * s),
-                                      umma_desc_sw128(p + part * F::kP + 32 * s), id_o,
-                                      j + part + s > 0 ? 1u : 0u);
+                    for (int s = 0; s < 4; ++s)  // 32 positions each
+                        umma_e4m3(tmem + F::o_col(buf), umma_desc_sw128(v + 32 * kDim * s),
+                                  umma_desc_mn(p + 32 * 16 * s, kTile * 16, 128), id_o,
+                                  j + s > 0 ? 1u : 0u);
                     umma_commit(&empty[stage]);
-                    umma_commit(&pempty[pslot]);
+                    umma_commit(&pempty[slot]);
                     advance();
-                    if (++pslot == F::kPSlots) {
-                        pslot = 0;
-                        pphase ^= 1;
+                    if (++pslot[h] == F::kGroupSlots) {
+                        pslot[h] = 0;
+                        pphase[h] ^= 1;
                     }
                 }
                 if (ok) umma_commit(&ofull[buf]);
                 ++gv;
             }
         }
+    } else if (warp == 2 + kFewSoftmaxWarps) {
+        // ------------------------------------------------------------ queries
+        // two E4M3 parts per row, K-major with the 128-byte swizzle; rows behind
+        // the segment's are zeros
+        const int sub = lane & 15, G = a.group;
+        uint32_t segs = 0;
+        bool ok = true;
+        while (ok && cur.next()) {
+            if (!cur.first) continue;
+            const uint32_t rb = (segs & 3) * NR;
+            const int rows = cur.seq.q_len * G;
+            uint4 v[NR / 2];
+#pragma unroll
+            for (int i = 0; i < NR / 2; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (r < rows) {
+                    const int tok = r / G, g = r - tok * G;
+                    v[i] = *reinterpret_cast<const uint4 *>(
+                        a.q + (cur.seq.q0 + tok) * a.q_stride +
+                        static_cast<int64_t>(cur.hk * G + g) * kDim + sub * 8);
+                }
+            }
+            ok = mbar_wait(&qempty[segs & 1], ((segs >> 1) & 1) ^ 1, abort_flag, status);
+            uint8_t *dst = smem + F::kQOff + (segs & 1) * F::kQ;
+#pragma unroll
+            for (int i = 0; i < NR / 2; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                uint32_t m = amax_bits8(v[i]);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                // power of two that takes the largest channel to [128, 256)
+                const int e = max(static_cast<int>(m >> 7) - 127, -100);
+                const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+                float f[8];
+                unpack_bf16x8(v[i], f);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x = f[2 * k] * up, y = f[2 * k + 1] * up;
+                    const uint16_t h = e4m3x2_satfinite(x, y);
+                    const float2 d = e4m3x2_to_float2(h);
+                    hi[k] = h;
+                    lo[k] = e4m3x2_satfinite(x - d.x, y - d.y);
+                }
+                // rows r and NR + r have the same place in their 8-row swizzle group
+                const int off = r * kDim + (((sub >> 1) ^ (r & 7)) << 4) + (sub & 1) * 8;
+                *reinterpret_cast<uint2 *>(dst + off) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+                *reinterpret_cast<uint2 *>(dst + NR * kDim + off) =
+                    make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+                if (sub == 0) {
+                    row_scale[rb + r] =
+                        a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+                    row_lim[rb + r] = a.causal
+                                          ? min(cur.seq.len - cur.seq.q_real + r / G, cur.seq.len - 1)
+                                          : cur.seq.len - 1;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&qfull[segs & 3]);
+            ++segs;
+        }
     } else {
         // ------------------------------------------------------------ softmax
         // A wait that gives up sets the abort flag: the loops then run to their
         // end without waiting, so that every barrier still has all its warps.
+        constexpr int kThreads = 32 * kFewSoftmaxWarps;
+        constexpr int kHalf = NR / 2;  // rows of a thread in the merge
         const int sw = warp - 2, st = threadIdx.x - 64;
-        const int quarter = warp & 3;
+        const int group = sw >> 2, quarter = warp & 3;
         const int lane_row = quarter * 32 + lane;  // position in a tile, channel of an output
         const uint32_t tm = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const int G = a.group;
@@ -419,303 +552,118 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const Seq s = seq_of(a, b);
             if (s.len > 0) continue;
             const int64_t width = static_cast<int64_t>(a.q_heads) * kDim;
-            for (int64_t i = st; i < s.q_len * width; i += 128)
+            for (int64_t i = st; i < s.q_len * width; i += kThreads)
                 a.out[(s.q0 + i / width) * a.out_stride + i % width] = 0;
             if (a.lse != nullptr)
-                for (int i = st; i < s.q_len * a.q_heads; i += 128)
+                for (int i = st; i < s.q_len * a.q_heads; i += kThreads)
                     a.lse[static_cast<int64_t>(s.q0) * a.q_heads + i] = -INFINITY;
         }
 
-        // Q of a segment: two E4M3 parts per row, K-major with the 128-byte swizzle
-        uint32_t qsegs = 0;
-        auto load_q = [&](const Chunks<N> &c) {
-            uint8_t *dst = smem + F::kQOff + (qsegs & 1) * 2 * F::kQ;
-            const int rows = c.seq.q_len * G;
-            const int sub = st & 15;
-            for (int r = st >> 4; r < N; r += 8) {
-                float f[8];
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    const int i = r / G, g = r - i * G;
-                    v = *reinterpret_cast<const uint4 *>(
-                        a.q + (c.seq.q0 + i) * a.q_stride +
-                        static_cast<int64_t>(c.hk * G + g) * kDim + sub * 8);
-                }
-                uint32_t m = amax_bits8(v);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                // power of two that takes the largest channel to [128, 256)
-                const int e = max(static_cast<int>(m >> 7) - 127, -100);
-                const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
-                unpack_bf16x8(v, f);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = f[2 * k] * up, y = f[2 * k + 1] * up;
-                    const uint16_t h = e4m3x2_satfinite(x, y);
-                    const float2 d = e4m3x2_to_float2(h);
-                    hi[k] = h;
-                    lo[k] = e4m3x2_satfinite(x - d.x, y - d.y);
-                }
-                const int off = r * kDim + (((sub >> 1) ^ (r & 7)) << 4) + (sub & 1) * 8;
-                *reinterpret_cast<uint2 *>(dst + off) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-                *reinterpret_cast<uint2 *>(dst + F::kQ + off) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-                if (sub == 0) {
-                    row_scale[(qsegs & 1) * N + r] =
-                        a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
-                    row_lim[(qsegs & 1) * N + r] =
-                        a.causal ? min(c.seq.len - c.seq.q_real + r / G, c.seq.len - 1) : c.seq.len - 1;
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&qfull[qsegs & 1]);
-            ++qsegs;
+        float l_run[NR];     // sums over this thread's positions
+        float o_run[kHalf];  // this thread's channel of rows group * kHalf ...
+        uint32_t g = 0, segs = 0, pslot = 0, pphase = 0, ragged = 0;
+        uint32_t vstage = 0;  // ring stage of the next V tile
+        Chunks<NR> ahead = cur;
+        bool more = ahead.next();
+        if (more) vstage = ahead.n % F::kStages;
+        // what the merge and the end of a segment need of the chunk before
+        struct {
+            int q0, hk, rows, tiles, seg_t0, seg_end;
+            int64_t item;
+            bool first, last;
+        } prev;
+
+        // Row r of a segment is token r / G, query head hk G + r % G.
+        auto out_at = [&](int r) {
+            const int i = r / G;
+            return a.out + (prev.q0 + i) * a.out_stride +
+                   static_cast<int64_t>(prev.hk * G + r - i * G) * kDim;
+        };
+        auto store_lse = [&](int r, float m, float l) {
+            const int i = r / G;
+            a.lse[static_cast<int64_t>(prev.q0 + i) * a.q_heads + prev.hk * G + r - i * G] =
+                l > 0.0f ? (m - kPScale + log2f(l)) * 0.69314718055994531f : -INFINITY;
         };
 
-        float o_run[N], l_run[N];  // this thread's channel; this thread's positions
-        uint32_t g = 0, pslot = 0, pphase = 0, segs = 0;
-        uint32_t vstage = 0;            // ring stage of the next V tile
-        uint32_t ragged = 0;            // tiles with an end so far
-        int rows = 0;
-
-        bool fresh = true;  // o_run holds nothing of the segment yet
-        auto merge = [&](uint32_t chunk) {  // O^T of a chunk into o_run
-            const uint32_t buf = chunk & 1;
-            mbar_wait(&ofull[buf], (chunk >> 1) & 1, abort_flag, status);
+        // O^T of chunk `c` into o_run; at the end of its segment, its output
+        auto merge = [&](uint32_t c) {
+            const uint32_t buf = c & 1;
+            float hi[kHalf], lo[kHalf];
+            mbar_wait(&ofull[buf], (c >> 1) & 1, abort_flag, status);
             tc_fence_after_sync();
-#pragma unroll
-            for (int c = 0; c < N; c += 16) {
-                if (c >= rows) break;
-                float v[16];
-                tmem_load16(tm + F::o_col(buf) + c, v);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o_run[c + k] = fresh ? v[k] : o_run[c + k] + v[k];
-            }
-            fresh = false;
+            tmem_ld<kHalf>(tm + F::o_col(buf) + group * kHalf, hi);
+            tmem_ld<kHalf>(tm + F::o_col(buf) + NR + group * kHalf, lo);
+            tmem_ld_wait<kHalf>(hi);
+            tmem_ld_wait<kHalf>(lo);
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ofree[buf]);
-        };
-
-        if (more) {
-            load_q(ahead);
-            vstage = ahead.n % F::kStages;
-        }
-        named_barrier(1, 128);
-        while (cur.next()) {
-            more = ahead.next();
-            if (more) {
-                if (ahead.first) load_q(ahead);
-                vstage = (vstage + ahead.n) % F::kStages;  // V of this chunk follows K of the next
+#pragma unroll
+            for (int k = 0; k < kHalf; ++k) {
+                const float o = hi[k] + lo[k];
+                o_run[k] = prev.first ? o : fmaf(o_run[k], row_fac[buf * NR + group * kHalf + k], o);
             }
-            if (cur.first) {
-                rows = cur.seq.q_len * G;
-                ++segs;
-            }
-            const float *scale = row_scale + ((segs - 1) & 1) * N;
-            const int *limit = row_lim + ((segs - 1) & 1) * N;
-            const uint32_t buf = g & 1;
-            // the first new token's last position: later ones are masked somewhere
-            const int q_real = cur.seq.q_real, len = cur.seq.len;
-            const int all_see = a.causal ? len - q_real : len - 1;
-            mbar_wait(&sfull[buf], (g >> 1) & 1, abort_flag, status);
-            tc_fence_after_sync();
-            // pass 1: the chunk's maximum of every row
-            float mx[N];
-#pragma unroll
-            for (int r = 0; r < N; ++r) mx[r] = -INFINITY;
-            for (int j = 0; j < cur.n; ++j) {
-                const int pos = (cur.t + j) * kTile + lane_row;
-                const bool plain = (cur.t + j) * kTile + kTile - 1 <= all_see;
-#pragma unroll
-                for (int c = 0; c < N; c += 16) {
-                    if (c >= rows) break;
-                    float v[16];
-                    tmem_load16(tm + F::s_col(buf, j) + c, v);
-                    if (plain) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) mx[c + k] = fmaxf(mx[c + k], v[k]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (pos <= limit[c + k]) mx[c + k] = fmaxf(mx[c + k], v[k]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < N; ++r) {
-                if (r >= rows) break;
-                const float m = warp_max(mx[r]);
-                if (lane == 0) row_red[sw * N + r] = m;
-            }
-            named_barrier(1, 128);
-            if (st < rows) {
-                float m = fmaxf(fmaxf(row_red[st], row_red[N + st]),
-                                fmaxf(row_red[2 * N + st], row_red[3 * N + st]));
-                m *= scale[st];  // -inf stays: nothing of the chunk is seen
-                const float old = cur.first ? -INFINITY : row_max[(buf ^ 1) * N + st];
-                m = fmaxf(m, old);
-                row_max[buf * N + st] = m;
-                row_neg[st] = m == -INFINITY ? 0.0f : kPScale - m;
-                row_fac[st] = m == -INFINITY ? 1.0f : ex2(old - m);
-            }
-            named_barrier(1, 128);
-            // the previous chunk's output, in the scale of its maximum, then both
-            // (and the sums) in the scale of this one's
-            if (cur.first) {
-                fresh = true;
-#pragma unroll
-                for (int r = 0; r < N; ++r) l_run[r] = 0.0f;
-            } else {
-                merge(g - 1);
-#pragma unroll
-                for (int r = 0; r < N; ++r) {
-                    if (r >= rows) break;
-                    const float f = row_fac[r];
-                    l_run[r] *= f;
-                    o_run[r] *= f;
-                }
-            }
-            // pass 2: weights, as two E4M3 parts, P[row][position]
-            for (int j = 0; j < cur.n; ++j) {
-                const int pos = (cur.t + j) * kTile + lane_row;
-                const bool plain = (cur.t + j) * kTile + kTile - 1 <= all_see;
-                mbar_wait(&pempty[pslot], pphase ^ 1, abort_flag, status);
-                uint8_t *p_hi = smem + F::kPOff + pslot * 2 * F::kP, *p_lo = p_hi + F::kP;
-#pragma unroll
-                for (int c = 0; c < N; c += 16) {
-                    if (c >= rows) break;
-                    float v[16];
-                    tmem_load16(tm + F::s_col(buf, j) + c, v);
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        if (c + k >= rows) break;
-                        float x = ex2(fmaf(v[k], scale[c + k], row_neg[c + k]));
-                        float y = ex2(fmaf(v[k + 1], scale[c + k + 1], row_neg[c + k + 1]));
-                        if (!plain) {
-                            if (pos > limit[c + k]) x = 0.0f;
-                            if (pos > limit[c + k + 1]) y = 0.0f;
-                        }
-                        l_run[c + k] += x;
-                        l_run[c + k + 1] += y;
-                        const uint16_t h = e4m3x2_satfinite(x, y);
-                        const float2 d = e4m3x2_to_float2(h);
-                        const uint16_t l = e4m3x2_satfinite(x - d.x, y - d.y);
-                        const int r = c + k, ch = lane_row >> 4, in = lane_row & 15;
-                        const int o0 = r * kTile + ((ch ^ (r & 7)) << 4) + in;
-                        const int o1 = (r + 1) * kTile + ((ch ^ ((r + 1) & 7)) << 4) + in;
-                        p_hi[o0] = static_cast<uint8_t>(h);
-                        p_hi[o1] = static_cast<uint8_t>(h >> 8);
-                        p_lo[o0] = static_cast<uint8_t>(l);
-                        p_lo[o1] = static_cast<uint8_t>(l >> 8);
-                    }
-                }
-                if ((cur.t + j) * kTile + kTile > len) {
-                    // the tile in which the sequence ends: what its page holds behind the
-                    // end may be NaN, which a weight of 0 would not silence
-                    mbar_wait(vready, ragged++ & 1, abort_flag, status);
-                    if (pos >= len) {
-                        uint4 *v = reinterpret_cast<uint4 *>(smem + vstage * kStageBytes + lane_row * kDim);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
-                    }
-                }
-                fence_proxy_async_smem();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&pfull[pslot]);
-                    if (j == cur.n - 1) mbar_arrive(&sfree[buf]);
-                }
-                if (++pslot == F::kPSlots) {
-                    pslot = 0;
-                    pphase ^= 1;
-                }
-                if (++vstage == F::kStages) vstage = 0;
-            }
-            ++g;
-            if (!cur.last) continue;
-
-            // ------------------------------------------------ end of a segment
-            merge(g - 1);
-#pragma unroll
-            for (int r = 0; r < N; ++r) {
-                if (r >= rows) break;
-                float l = l_run[r];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-                if (lane == 0) row_sum[sw * N + r] = l;
-            }
-            named_barrier(1, 128);
-            const float *m_row = row_max + buf * N;
+            if (!prev.last) return;
+            const int rows = prev.rows;
+            const float *m_row = row_max + buf * NR, *sums = row_sum + buf * 8 * NR;
             auto total = [&](int r) {
-                return (row_sum[r] + row_sum[N + r]) + (row_sum[2 * N + r] + row_sum[3 * N + r]);
-            };
-            // row r is token r / G, query head hk G + r % G
-            auto out_at = [&](int r) {
-                const int i = r / G;
-                return a.out + (cur.seq.q0 + i) * a.out_stride +
-                       static_cast<int64_t>(cur.hk * G + r - i * G) * kDim;
-            };
-            auto store_lse = [&](int r, float m, float l) {
-                const int i = r / G;
-                a.lse[static_cast<int64_t>(cur.seq.q0 + i) * a.q_heads + cur.hk * G + r - i * G] =
-                    l > 0.0f ? (m - kPScale + log2f(l)) * 0.69314718055994531f : -INFINITY;
-            };
-            if (cur.seg_t0 == 0 && cur.seg_end == cur.tiles) {
+                float l = 0.0f;
 #pragma unroll
-                for (int r = 0; r < N; ++r) {
+                for (int w = 0; w < kFewSoftmaxWarps; ++w) l += sums[w * NR + r];
+                return l;
+            };
+            if (prev.seg_t0 == 0 && prev.seg_end == prev.tiles) {
+#pragma unroll
+                for (int k = 0; k < kHalf; ++k) {
+                    const int r = group * kHalf + k;
                     if (r >= rows) break;
                     const float l = total(r);
                     out_at(r)[lane_row] = __bfloat16_as_ushort(
-                        __float2bfloat16_rn(l > 0.0f ? __fdividef(o_run[r], l) : 0.0f));
+                        __float2bfloat16_rn(l > 0.0f ? __fdividef(o_run[k], l) : 0.0f));
                 }
                 if (a.lse != nullptr && st < rows) store_lse(st, m_row[st], total(st));
-                named_barrier(1, 128);  // row_sum and row_max are read
-                continue;
+                return;
             }
             // partial: this CTA's slot 1 if the (sequence, head) begins here, else slot 0
-            const int64_t all = start_w[3], w_first = cur.item(), w_last = w_first + cur.tiles - 1;
-            auto owner = [&](int64_t w) {
-                return static_cast<int>(((w + 1) * *parts - 1) / all);
-            };
+            const int64_t all = start_w[3], w_first = prev.item, w_last = w_first + prev.tiles - 1;
+            auto owner = [&](int64_t w) { return static_cast<int>(((w + 1) * *parts - 1) / all); };
             const int c_first = owner(w_first), c_last = owner(w_last);
-            auto slot = [&](int c) {
-                return partials + static_cast<int64_t>(2 * c + (c == c_first ? 1 : 0)) * F::kPartial;
+            auto slot = [&](int i) {
+                return partials + static_cast<int64_t>(2 * i + (i == c_first ? 1 : 0)) * F::kPartial;
             };
             float *mine = slot(blockIdx.x);
 #pragma unroll
-            for (int r = 0; r < N; ++r) {
+            for (int k = 0; k < kHalf; ++k) {
+                const int r = group * kHalf + k;
                 if (r >= rows) break;
-                __stcg(mine + r * kDim + lane_row, o_run[r]);
+                __stcg(mine + r * kDim + lane_row, o_run[k]);
             }
             if (st < rows) {
-                __stcg(mine + N * kDim + st, m_row[st]);
-                __stcg(mine + N * kDim + N + st, total(st));
+                __stcg(mine + NR * kDim + st, m_row[st]);
+                __stcg(mine + NR * kDim + NR + st, total(st));
             }
             __threadfence();
-            named_barrier(1, 128);
+            named_barrier(1, kThreads);
             if (st == 0) {
                 const int seen = atomicAdd(counters + c_first, 1);
                 *shared_last = seen == c_last - c_first;
                 if (*shared_last) counters[c_first] = 0;
                 __threadfence();
             }
-            named_barrier(1, 128);
-            if (!*shared_last) continue;
+            named_barrier(1, kThreads);
+            if (!*shared_last) return;
             // join in the order of the CTAs: a warp per row, 4 channels per lane
-            for (int r = sw; r < rows; r += 4) {
+            for (int r = sw; r < rows; r += kFewSoftmaxWarps) {
                 float m = -INFINITY, l = 0.0f;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int c = c_first; c <= c_last; ++c) m = fmaxf(m, __ldcg(slot(c) + N * kDim + r));
+                for (int i = c_first; i <= c_last; ++i) m = fmaxf(m, __ldcg(slot(i) + NR * kDim + r));
                 if (m > -INFINITY) {
 #pragma unroll 4
-                    for (int c = c_first; c <= c_last; ++c) {
-                        const float *p = slot(c);
-                        const float f = ex2(__ldcg(p + N * kDim + r) - m);
+                    for (int i = c_first; i <= c_last; ++i) {
+                        const float *p = slot(i);
+                        const float f = ex2(__ldcg(p + NR * kDim + r) - m);
                         const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + r * kDim) + lane);
-                        l = fmaf(f, __ldcg(p + N * kDim + N + r), l);
+                        l = fmaf(f, __ldcg(p + NR * kDim + NR + r), l);
                         o.x = fmaf(f, v.x, o.x);
                         o.y = fmaf(f, v.y, o.y);
                         o.z = fmaf(f, v.z, o.z);
@@ -727,7 +675,157 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
                 if (a.lse != nullptr && lane == 0) store_lse(r, m, l);
             }
+        };
+
+        while (cur.next()) {
+            more = ahead.next();
+            if (more) vstage = (vstage + ahead.n) % F::kStages;  // V of this chunk follows K of the next
+            const uint32_t buf = g & 1;
+            const int rows = cur.seq.q_len * G, len = cur.seq.len;
+            if (cur.first) {
+                mbar_wait(&qfull[segs & 3], (segs >> 2) & 1, abort_flag, status);
+                ++segs;
+            }
+            const float *scale = row_scale + ((segs - 1) & 3) * NR;
+            const int *limit = row_lim + ((segs - 1) & 3) * NR;
+            // positions that every row sees; later ones are masked somewhere
+            const int all_see = a.causal ? len - cur.seq.q_real : len - 1;
+            mbar_wait(&sfull[buf], (g >> 1) & 1, abort_flag, status);
+            tc_fence_after_sync();
+
+            // scores of tile j, rows [c, c + X): hi + lo
+            auto load_scores = [&](int j, auto &v) {
+                float lo[NR];
+#pragma unroll
+                for (int c = 0; c < NR; c += NR < 16 ? NR : 16) {
+                    tmem_ld<NR < 16 ? NR : 16>(tm + F::s_col(buf, j) + c, v + c);
+                    tmem_ld<NR < 16 ? NR : 16>(tm + F::s_col(buf, j) + NR + c, lo + c);
+                }
+                tmem_ld_wait<NR>(v);
+                tmem_ld_wait<NR>(lo);
+#pragma unroll
+                for (int r = 0; r < NR; ++r) v[r] += lo[r];
+            };
+
+            // pass 1: the chunk's maximum of every row
+            float mx[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
+            for (int j = group; j < cur.n; j += 2) {
+                const int pos = (cur.t + j) * kTile + lane_row;
+                float v[NR];
+                load_scores(j, v);
+                if ((cur.t + j) * kTile + kTile - 1 <= all_see) {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) mx[r] = fmaxf(mx[r], v[r]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        if (pos <= limit[r]) mx[r] = fmaxf(mx[r], v[r]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float m = warp_max(mx[r]);
+                if (lane == 0) row_red[sw * NR + r] = m;
+            }
+            named_barrier(1, kThreads);
+            if (st < NR) {
+                float m = row_red[st];
+#pragma unroll
+                for (int w = 1; w < kFewSoftmaxWarps; ++w) m = fmaxf(m, row_red[w * NR + st]);
+                m *= scale[st];  // -inf stays: nothing of the chunk is seen
+                const float old = cur.first ? -INFINITY : row_max[(buf ^ 1) * NR + st];
+                m = fmaxf(m, old);
+                row_max[buf * NR + st] = m;
+                row_neg[st] = m == -INFINITY ? 0.0f : kPScale - m;
+                row_fac[buf * NR + st] = m == -INFINITY ? 1.0f : ex2(old - m);
+            }
+            named_barrier(1, kThreads);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l_run[r] = cur.first ? 0.0f : l_run[r] * row_fac[buf * NR + r];
+
+            // pass 2: weights, two E4M3 parts, P[position][hi rows, lo rows]
+            for (int j = group; j < cur.n; j += 2) {
+                const int pos = (cur.t + j) * kTile + lane_row;
+                float v[NR];
+                load_scores(j, v);
+#pragma unroll
+                for (int r = 0; r < NR; ++r) v[r] = ex2(fmaf(v[r], scale[r], row_neg[r]));
+                if ((cur.t + j) * kTile + kTile - 1 > all_see) {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        if (pos > limit[r]) v[r] = 0.0f;
+                }
+                uint32_t hi[NR / 4], lo[NR / 4];
+#pragma unroll
+                for (int r = 0; r < NR; r += 4) {
+                    const uint16_t h0 = e4m3x2_satfinite(v[r], v[r + 1]);
+                    const uint16_t h1 = e4m3x2_satfinite(v[r + 2], v[r + 3]);
+                    const float2 d0 = e4m3x2_to_float2(h0), d1 = e4m3x2_to_float2(h1);
+                    hi[r / 4] = h0 | (static_cast<uint32_t>(h1) << 16);
+                    lo[r / 4] = e4m3x2_satfinite(v[r] - d0.x, v[r + 1] - d0.y) |
+                                (static_cast<uint32_t>(e4m3x2_satfinite(v[r + 2] - d1.x, v[r + 3] - d1.y)) << 16);
+                }
+#pragma unroll
+                for (int r = 0; r < NR; ++r) l_run[r] += v[r];
+                const uint32_t slot = group * F::kGroupSlots + pslot;
+                mbar_wait(&pempty[slot], pphase ^ 1, abort_flag, status);
+                uint4 *p = reinterpret_cast<uint4 *>(smem + F::kPOff + slot * F::kP) + lane_row;
+                if constexpr (NR == 8) {
+                    *p = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NR / 16; ++c) {
+                        p[c * kTile] = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                        p[(NR / 16 + c) * kTile] = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                    }
+                }
+                if ((cur.t + j + 1) * kTile > len) {
+                    // the tile in which the sequence ends: what its page holds behind the
+                    // end may be NaN, which a weight of 0 would not silence
+                    mbar_wait(&vready[group], ragged++ & 1, abort_flag, status);
+                    if (pos >= len) {
+                        uint4 *z = reinterpret_cast<uint4 *>(smem + (vstage + j) % F::kStages * kStageBytes + lane_row * kDim);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) z[k] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[slot]);
+                if (++pslot == F::kGroupSlots) {
+                    pslot = 0;
+                    pphase ^= 1;
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfree[buf]);
+            vstage = (vstage + cur.n) % F::kStages;
+            if (cur.last) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    float l = l_run[r];
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+                    if (lane == 0) row_sum[(buf * 8 + sw) * NR + r] = l;
+                }
+            }
+            if (g > 0) merge(g - 1);
+            prev.q0 = cur.seq.q0;
+            prev.hk = cur.hk;
+            prev.rows = rows;
+            prev.tiles = cur.tiles;
+            prev.seg_t0 = cur.seg_t0;
+            prev.seg_end = cur.seg_end;
+            prev.item = cur.item();
+            prev.first = cur.first;
+            prev.last = cur.last;
+            ++g;
         }
+        named_barrier(1, kThreads);  // row_sum of the last chunk
+        if (g > 0) merge(g - 1);
     }
     tc_fence_before_sync();
     __syncthreads();

@@ -248,8 +248,8 @@ const DeviceInfo *device_info() {
                                  attn::Few<16>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(attn::attention_few_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  attn::Few<32>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(attn::attention_few_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 attn::Few<64>::kBytes) != cudaSuccess)
+            cudaFuncSetAttribute(attn::attention_few_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 attn::Few<8>::kBytes) != cudaSuccess)
             return;
         for (int c = 2; c <= 8; ++c) {
             cudaLaunchConfig_t cfg = {};
@@ -718,22 +718,22 @@ int64_t attention_rows(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max
     return std::min(max_q_len, T) * (q_heads / kv_heads);
 }
 
-template <int N>
+template <int NR>
 size_t few_ws_bytes() {
-    return round256(decode::kCounterBytes + int64_t(2) * decode::kMaxGrid * attn::Few<N>::kPartial * 4);
+    return round256(decode::kCounterBytes + int64_t(2) * decode::kMaxGrid * attn::Few<NR>::kPartial * 4);
 }
 
 size_t attention_ws_bytes(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_q_len) {
     const int64_t rows = attention_rows(T, q_heads, kv_heads, max_q_len);
-    return rows <= 16 ? few_ws_bytes<16>() : rows <= 32 ? few_ws_bytes<32>() : rows <= 64 ? few_ws_bytes<64>() : 0;
+    return rows <= 8 ? few_ws_bytes<8>() : rows <= 16 ? few_ws_bytes<16>() : rows <= 32 ? few_ws_bytes<32>() : 0;
 }
 
-template <int N>
+template <int NR>
 cudaError_t launch_few(const DeviceInfo &d, const attn::Args &a, const CUtensorMap &tk,
                        const CUtensorMap &tv, void *ws, cudaStream_t st) {
     const int grid = std::min<int>(d.sm_count, decode::kMaxGrid);
-    return launch(attn::attention_few_kernel<N>, dim3(static_cast<unsigned>(grid)),
-                  dim3(attn::kFewThreads), attn::Few<N>::kBytes, st, tk, tv, a,
+    return launch(attn::attention_few_kernel<NR>, dim3(static_cast<unsigned>(grid)),
+                  dim3(attn::kFewThreads), attn::Few<NR>::kBytes, st, tk, tv, a,
                   static_cast<int *>(ws),
                   reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + decode::kCounterBytes),
                   d.status);
@@ -742,7 +742,7 @@ cudaError_t launch_few(const DeviceInfo &d, const attn::Args &a, const CUtensorM
 fp8bq_status launch_attention(const DeviceInfo &d, const attn::Args &a, int64_t num_slots, void *ws,
                               cudaStream_t st) {
     const int64_t rows = int64_t(a.max_q) * a.group;
-    if (rows <= 64) {
+    if (rows <= 32) {
         // without a slot there is nothing to map: any descriptor will do, no
         // page is in the cache
         CUtensorMap tk, tv;
@@ -755,9 +755,9 @@ fp8bq_status launch_attention(const DeviceInfo &d, const attn::Args &a, int64_t 
             !make_tmap_2d(&tv, v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, slots, a.slot_stride, attn::kDim,
                           box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
             return FP8BQ_ERR_CUDA;
-        return from_cuda(rows <= 16   ? launch_few<16>(d, a, tk, tv, ws, st)
-                         : rows <= 32 ? launch_few<32>(d, a, tk, tv, ws, st)
-                                      : launch_few<64>(d, a, tk, tv, ws, st));
+        return from_cuda(rows <= 8    ? launch_few<8>(d, a, tk, tv, ws, st)
+                         : rows <= 16 ? launch_few<16>(d, a, tk, tv, ws, st)
+                                      : launch_few<32>(d, a, tk, tv, ws, st));
     }
     return from_cuda(launch(attn::attention_simple_kernel,
                             dim3(static_cast<unsigned>(a.T * a.q_heads)),
