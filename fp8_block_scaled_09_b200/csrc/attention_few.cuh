@@ -177,18 +177,44 @@ __device__ __forceinline__ int seq_tiles(const Seq &s) {
     return s.q_len > 0 ? (s.len + kTile - 1) / kTile : 0;
 }
 
-// Row of the cache where page `idx` of sequence b starts, or -kTile (a row
-// outside the cache: TMA fills zeros) for a page it does not need or that is
-// not in the cache.
-__device__ __forceinline__ int page_row(const Args &a, int b, int idx, int len, int *status) {
-    if ((static_cast<int64_t>(idx) << a.page_shift) >= len) return -kTile;
-    const int32_t page = __ldg(a.table + b * a.table_stride + idx);
-    if (page < 0 || page >= a.num_pages) {
-        atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
-        return -kTile;
+// The pages of a sequence as a producer warp walks them: lane l holds entry
+// l of the current and of the next 32 (loaded before they are needed: a line of
+// the table that is still in HBM costs a microsecond).
+struct PageWalk {
+    const int32_t *row;
+    int blk, n, cur, nxt;
+
+    __device__ int load(int b) const {
+        const int i = b * 32 + static_cast<int>(threadIdx.x & 31);
+        return i < n ? __ldg(row + i) : -1;
     }
-    return page << a.page_shift;
-}
+    // to be read from position `pos` on, up to the sequence's length
+    __device__ PageWalk(const Args &a, int b, int len, int pos)
+        : row(a.table + b * a.table_stride), blk((pos >> a.page_shift) >> 5),
+          n((len + (1 << a.page_shift) - 1) >> a.page_shift) {
+        cur = load(blk);
+        nxt = load(blk + 1);
+    }
+    // Warp-wide: first cache row of position `pos` (ascending calls; every lane's
+    // in the same 32 pages), or -kTile (a row outside the cache: TMA fills
+    // zeros) for a page that is not needed or not in the cache.
+    __device__ int row_of(const Args &a, int pos, int *status) {
+        const int idx = pos >> a.page_shift;
+        const int want = __shfl_sync(0xFFFFFFFFu, idx >> 5, 0);
+        if (want != blk) {
+            blk = want;
+            cur = nxt;
+            nxt = load(blk + 1);
+        }
+        const int page = __shfl_sync(0xFFFFFFFFu, cur, idx & 31);
+        if (idx >= n) return -kTile;
+        if (page < 0 || page >= a.num_pages) {
+            atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
+            return -kTile;
+        }
+        return (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+    }
+};
 
 // Positions of the work list that one head of a sequence takes.
 __device__ __forceinline__ int64_t head_cost(int tiles) {
@@ -352,21 +378,13 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
         Chunks<NR> ahead = cur;  // the chunk whose K comes next
         bool more = ahead.next();
         const uint64_t evict_first = l2_policy_evict_first();
-        const int page = 1 << a.page_shift;
-        const int rows = min(page, kTile), boxes = kTile / rows;
+        const int rows = min(1 << a.page_shift, kTile), boxes = kTile / rows;
         uint32_t stage = 0, phase = 0, issued = 0;
         bool ok = true;
         auto tiles = [&](const Chunks<NR> &c, const CUtensorMap *map) {
-            // the next tile's page while this one waits for its slot
-            auto row_at = [&](int t) {
-                if (lane >= boxes || t >= c.t + c.n) return -kTile;
-                const int pos = t * kTile + lane * rows;
-                const int r = page_row(a, c.b, pos >> a.page_shift, c.seq.len, status);
-                return r < 0 ? r : r + (pos & (page - 1));
-            };
-            int row = row_at(c.t);
+            PageWalk pages(a, c.b, c.seq.len, c.t * kTile);
             for (int t = c.t; t < c.t + c.n; ++t) {
-                const int next_row = row_at(t + 1);
+                const int row = pages.row_of(a, t * kTile + min(lane, boxes - 1) * rows, status);
                 ok = ok && mbar_wait(&empty[stage], phase ^ 1, abort_flag, status);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
@@ -377,7 +395,6 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (lane < boxes)
                     tma_load_2d_hint(smem + stage * kStageBytes + lane * rows * kDim, map,
                                      &full[stage], c.hk * kDim, row, evict_first);
-                row = next_row;
                 ++issued;
                 if (++stage == F::kStages) {
                     stage = 0;
@@ -496,17 +513,22 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             ok = mbar_wait(&qempty[segs & 1], ((segs >> 1) & 1) ^ 1, abort_flag, status);
             uint8_t *dst = smem + F::kQOff + (segs & 1) * F::kQ;
-#pragma unroll
+            // not unrolled (the rows move down the array instead): unrolled, the
+            // first pass over this code fetched it for 4 us before the first MMA
+#pragma unroll 1
             for (int i = 0; i < NR / 2; ++i) {
                 const int r = 2 * i + (lane >> 4);
-                uint32_t m = amax_bits8(v[i]);
+                const uint4 u = v[0];
+#pragma unroll
+                for (int k = 0; k + 1 < NR / 2; ++k) v[k] = v[k + 1];
+                uint32_t m = amax_bits8(u);
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
                 // power of two that takes the largest channel to [128, 256)
                 const int e = max(static_cast<int>(m >> 7) - 127, -100);
                 const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
                 float f[8];
-                unpack_bf16x8(v[i], f);
+                unpack_bf16x8(u, f);
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -652,22 +674,38 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             named_barrier(1, kThreads);
             if (!*shared_last) return;
-            // join in the order of the CTAs: a warp per row, 4 channels per lane
+            // join in the order of the CTAs: a warp per row, 4 channels per lane;
+            // 32 CTAs' maxima and sums at a time, one per lane
             for (int r = sw; r < rows; r += kFewSoftmaxWarps) {
                 float m = -INFINITY, l = 0.0f;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int i = c_first; i <= c_last; ++i) m = fmaxf(m, __ldcg(slot(i) + NR * kDim + r));
-                if (m > -INFINITY) {
-#pragma unroll 4
-                    for (int i = c_first; i <= c_last; ++i) {
-                        const float *p = slot(i);
-                        const float f = ex2(__ldcg(p + NR * kDim + r) - m);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + r * kDim) + lane);
-                        l = fmaf(f, __ldcg(p + NR * kDim + NR + r), l);
-                        o.x = fmaf(f, v.x, o.x);
-                        o.y = fmaf(f, v.y, o.y);
-                        o.z = fmaf(f, v.z, o.z);
-                        o.w = fmaf(f, v.w, o.w);
+                for (int i0 = c_first; i0 <= c_last; i0 += 32) {
+                    const int n = min(32, c_last - i0 + 1);
+                    const float *p = slot(min(i0 + lane, c_last)) + NR * kDim + r;
+                    float mi = lane < n ? __ldcg(p) : -INFINITY;
+                    const float li = lane < n ? __ldcg(p + NR) : 0.0f;
+                    const float m2 = fmaxf(m, warp_max(mi));
+                    if (m2 == -INFINITY) continue;
+                    const float f_old = ex2(m - m2), f = ex2(mi - m2);
+                    m = m2;
+                    float part = li * f;
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
+                    l = fmaf(l, f_old, part);
+                    o = make_float4(o.x * f_old, o.y * f_old, o.z * f_old, o.w * f_old);
+                    for (int i = 0; i < n; i += 8) {
+                        float4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = __ldcg(reinterpret_cast<const float4 *>(slot(i0 + min(i + k, n - 1)) + r * kDim) + lane);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float fi = i + k < n ? __shfl_sync(0xFFFFFFFFu, f, i + k) : 0.0f;
+                            o.x = fmaf(fi, v[k].x, o.x);
+                            o.y = fmaf(fi, v[k].y, o.y);
+                            o.z = fmaf(fi, v[k].z, o.z);
+                            o.w = fmaf(fi, v[k].w, o.w);
+                        }
                     }
                 }
                 const float inv = l > 0.0f ? __fdividef(1.0f, l) : 0.0f;
