@@ -1,0 +1,731 @@
+// attention_many.cuh -- paged attention for many query rows per kv head (prefill
+// chunks, blocks of new tokens).
+//
+// A sequence's query rows of one kv head, r = token * group + head, are taken
+// 256 at a time, as two halves A and B of 128 rows that share every K and V
+// tile of 128 positions:
+//     S[row, pos] = Q[row, :] . K[pos, :]      E4M3, M = N = 128, K = 128, twice
+//     O[row, ch] += P[row, :] . V[:, ch]       F16,  M = N = 128, K = 128
+// K is never converted: a BF16 query row is held as two E4M3 parts hi + lo (see
+// attention_few.cuh), two MMAs at twice the 16-bit rate.  V becomes F16 (exact, as
+// 2^-8 V: an E4M3 code's bits moved into an F16 are its value times 2^-8, so
+// four integer instructions convert two codes; the output takes the 2^8 back).
+// P is F16 too, 11 bits, and never leaves the tensor memory: it replaces the
+// scores it came from and is the A operand of the second product.
+//
+// Bound by the tensor pipe, 1024 cycles per half and tile, and equally by the
+// exponentials (16 a cycle and SM: 1024 cycles per half and tile): the halves
+// alternate, one's softmax under the other's MMAs.  A softmax thread has a whole
+// row, so maxima and sums need no exchange.  The running maximum is only
+// moved when a row's scores pass it by 2^8 (weights up to 2^8 are as exact in
+// F16 and FP32), so O is hardly ever rescaled in the tensor memory.
+//
+// Work is a list of K/V tiles ordered by (sequence, 256 rows, kv head, tile),
+// each (rows, head) item preceded by kItemCost tiles' worth of nothing; CTA c of
+// one per SM takes the c-th equal part, so that neither causal masks nor lengths
+// nor a last wave leave SMs idle.  An item that lies in several CTAs is joined
+// as in attention_few.cuh, each half by itself.
+//
+// Roles (512 threads): warpgroups 0 and 1 softmax of A and B (192 registers a
+// thread: 128 scores), 2 converts V, warp 12 TMA producer, warp 13 MMA issuer.
+#pragma once
+
+#include "attention_few.cuh"
+
+namespace fp8bq {
+namespace attn {
+
+constexpr int kManyThreads = 512;
+constexpr int kManyLaunchRegs = 128;
+constexpr int kSoftmaxRegs = 192, kConvertRegs = 72, kIssueRegs = 56;
+static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <=
+                  kManyThreads * kManyLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr int kItemCost = 3;      // tiles' worth of work that an item adds
+constexpr int kManyMaxGrid = 160;
+constexpr int kHalfRows = 128;
+constexpr float kRescaleAt = 8.0f;  // log2
+
+struct Many {
+    static constexpr int kStages = 6;  // K tiles in even, V tiles in odd stages
+    static constexpr int kQPart = kHalfRows * kDim;   // 16 KB
+    static constexpr int kRingOff = 4 * kQPart;       // Q: [half][hi, lo]
+    static constexpr int kV16 = kTile * kDim * 2;     // 32 KB
+    static constexpr int kV16Off = kRingOff + kStages * kStageBytes;
+    static constexpr int kBarOff = kV16Off + 2 * kV16;
+    // full, empty; vfull, vempty, qfull, sfull, pfull, ofull (two each)
+    static constexpr int kBars = 2 * kStages + 12;
+    static constexpr int kMiscOff = kBarOff + kBars * 8;
+    static constexpr int kBytes = kMiscOff + 256 + 1024;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    // floats of one half's partial: O [32 groups of 4 channels][128 rows][4], max, sum [128]
+    static constexpr int kPartial = kHalfRows * (kDim + 2);
+    // TMEM columns
+    __device__ static uint32_t s_col(int half) { return half * 128; }
+    __device__ static uint32_t o_col(int half) { return 256 + half * 128; }
+};
+
+// A: E4M3 or F16 rows, both K-major; B of the second product: N contiguous.
+__host__ __device__ constexpr uint32_t idesc_f16_b_mn(int m, int n) {
+    return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// 128-byte-swizzled operand tile whose N dimension is contiguous: 64 F16 of N per
+// 128-byte row, 8 K rows per 1024-byte block, `n_step` bytes to the next 64 of N.
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t n_step) {
+    return (umma_desc_sw128(saddr) & ~(static_cast<uint64_t>(0x3FFF) << 16)) |
+           (static_cast<uint64_t>(n_step >> 4) << 16);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem] over K = 16 (F16; A two values per column).
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 consecutive columns of this warp's lanes, without the wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
+    return *reinterpret_cast<const float2 *>(&d);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two E4M3 codes in the high bytes of x's halves -> two F16 of 2^-8 their values.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16_shifted(uint32_t x) {
+    return (x & 0x80008000u) | ((x >> 1) & 0x3F803F80u);
+}
+
+// ------------------------------------------------------------------ work list
+
+// Last position that row r of a sequence sees (-1 or less: none).
+__device__ __forceinline__ int row_limit(const Args &a, const Seq &s, int r) {
+    return a.causal ? min(s.len - s.q_real + r / a.group, s.len - 1) : s.len - 1;
+}
+
+// 256-row blocks of a sequence with positions.
+__device__ __forceinline__ int row_blocks(const Args &a, const Seq &s) {
+    return s.len > 0 ? (s.q_len * a.group + 255) / 256 : 0;
+}
+
+// K/V tiles that rows [.., end) of a sequence need (at least one, which then
+// masks everything).
+__device__ __forceinline__ int tiles_until(const Args &a, const Seq &s, int end) {
+    return max(row_limit(a, s, min(end, s.q_len * a.group) - 1) / kTile + 1, 1);
+}
+
+// Cost of all items of a sequence (warp-wide, the same in every lane).
+__device__ __forceinline__ int64_t seq_cost(const Args &a, const Seq &s) {
+    const int blocks = row_blocks(a, s);
+    int64_t c = 0;
+    for (int m = threadIdx.x & 31; m < blocks; m += 32) c += tiles_until(a, s, m * 256 + 256) + kItemCost;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+    return c * a.kv_heads;
+}
+
+// The segments of one CTA's part of the work list, in order.
+struct Items {
+    const Args &a;
+    int64_t w, w_end, base;  // next position, end of the part, first position of block m
+    int b, m, blocks;        // sequence and 256-row block of w
+    Seq seq;
+    int cost;                // positions of one head's item of block m
+    // the current segment
+    int hk, t0, t1;          // kv head, tiles [t0, t1)
+    int tiles, tiles_a;      // of the whole item; of its half A
+    int rows;                // of the item, 1 .. 256
+
+    __device__ Items(const Args &args, int64_t w0, int64_t w1, int b0, int m0, int64_t base0)
+        : a(args), w(w0), w_end(w1), base(base0), b(b0), m(m0), blocks(0), cost(0), hk(0), t0(0),
+          t1(0), tiles(0), tiles_a(0), rows(0) {
+        if (w < w_end) {
+            seq = seq_of(a, b);
+            blocks = row_blocks(a, seq);
+            cost = tiles_until(a, seq, m * 256 + 256) + kItemCost;
+        }
+    }
+    __device__ bool next() {
+        for (;;) {
+            if (w >= w_end) return false;
+            while (w >= base + static_cast<int64_t>(cost) * a.kv_heads) {
+                base += static_cast<int64_t>(cost) * a.kv_heads;
+                if (++m >= blocks) {
+                    m = 0;
+                    do {
+                        seq = seq_of(a, ++b);
+                        blocks = row_blocks(a, seq);
+                    } while (blocks == 0);
+                }
+                cost = tiles_until(a, seq, m * 256 + 256) + kItemCost;
+            }
+            const int rel = static_cast<int>((w - base) % cost);
+            hk = static_cast<int>((w - base) / cost);
+            const int64_t left = min(static_cast<int64_t>(cost - rel), w_end - w);
+            t0 = max(rel - kItemCost, 0);
+            t1 = max(static_cast<int>(rel + left) - kItemCost, 0);
+            w += left;
+            if (t1 > t0) break;
+        }
+        tiles = cost - kItemCost;
+        tiles_a = tiles_until(a, seq, m * 256 + 128);
+        rows = min(seq.q_len * a.group - m * 256, 256);
+        return true;
+    }
+    __device__ bool has_b() const { return rows > kHalfRows; }
+    // tiles of a half in this segment
+    __device__ int count(int half) const {
+        return half == 0 ? max(min(t1, tiles_a) - t0, 0) : has_b() ? t1 - t0 : 0;
+    }
+    __device__ int64_t item() const { return base + static_cast<int64_t>(hk) * cost + kItemCost; }
+};
+
+// ------------------------------------------------------------------ kernel
+
+__global__ void __launch_bounds__(kManyThreads, 1)
+attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const Args a, int *counters,
+                      float *partials, int *status) {
+    using F = Many;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + F::kBarOff);
+    uint64_t *empty = full + F::kStages;
+    uint64_t *vfull = empty + F::kStages, *vempty = vfull + 2, *qfull = vempty + 2,
+             *sfull = qfull + 2, *pfull = sfull + 2, *ofull = pfull + 2;
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + F::kMiscOff);
+    uint32_t *tmem_slot = misc;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
+    int *shared_last = reinterpret_cast<int *>(misc + 2);      // [2]
+    int *start_bm = reinterpret_cast<int *>(misc + 4);         // sequence, block
+    int *parts = reinterpret_cast<int *>(misc + 6);            // CTAs that have a part
+    int64_t *start_w = reinterpret_cast<int64_t *>(misc + 8);  // w0, w1, base, total
+    int64_t *warp_cost = start_w + 4;                          // [16]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    allow_dependent_launch();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < F::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], i % 2 == 0 ? 1 : 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&vfull[i], 4);
+            mbar_init(&vempty[i], 1);
+            mbar_init(&qfull[i], 4);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+            mbar_init(&ofull[i], 1);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tmap_k);
+        prefetch_tmap(&tmap_v);
+    }
+    if (warp == 13) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    {
+        // this CTA's part of the work list: warp w sums the costs of the w-th run
+        // of sequences, then the warp whose run holds the first position finds it
+        const int per = (a.B + 15) / 16, b0 = min(warp * per, a.B), b1 = min(b0 + per, a.B);
+        int64_t mine = 0;
+        for (int b = b0; b < b1; ++b) mine += seq_cost(a, seq_of(a, b));
+        if (lane == 0) warp_cost[warp] = mine;
+        __syncthreads();
+        int64_t before = 0, total = 0;
+        for (int i = 0; i < 16; ++i) {
+            if (i < warp) before += warp_cost[i];
+            total += warp_cost[i];
+        }
+        // no part is empty, so that a split item lies in consecutive CTAs
+        const int64_t np = min(static_cast<int64_t>(gridDim.x), max(total, int64_t(1)));
+        const int64_t w0 = min(blockIdx.x * total / np, total), w1 = min((blockIdx.x + 1) * total / np, total);
+        if (w0 >= before && w0 < before + mine) {
+            int b = b0;
+            Seq s = seq_of(a, b);
+            for (;;) {
+                const int64_t n = seq_cost(a, s);
+                if (w0 < before + n) break;
+                before += n;
+                s = seq_of(a, ++b);
+            }
+            // the block: 32 at a time, an inclusive scan of their costs
+            int m = 0;
+            for (;; m += 32) {
+                const int blocks = row_blocks(a, s);
+                const int64_t c = m + lane < blocks
+                                      ? static_cast<int64_t>(tiles_until(a, s, (m + lane) * 256 + 256) + kItemCost) * a.kv_heads
+                                      : 0;
+                int64_t incl = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                    if (lane >= o) incl += up;
+                }
+                const unsigned hit = __ballot_sync(0xFFFFFFFFu, w0 < before + incl);
+                if (hit != 0) {
+                    const int l = __ffs(hit) - 1;
+                    if (lane == l) {
+                        start_bm[0] = b;
+                        start_bm[1] = m + l;
+                        start_w[2] = before + incl - c;
+                    }
+                    break;
+                }
+                before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            }
+        }
+        if (threadIdx.x == 0) {
+            start_w[0] = w0;
+            start_w[1] = w1;
+            start_w[3] = total;
+            *parts = static_cast<int>(np);
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    Items it(a, start_w[0], start_w[1], start_bm[0], start_bm[1], start_w[2]);
+
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == 12) {
+            // -------------------------------------------------------- producer
+            const int rows = min(1 << a.page_shift, kTile), boxes = kTile / rows;
+            uint32_t stage = 0, phase = 0, issued = 0;
+            bool ok = true;
+            while (ok && it.next()) {
+                PageWalk pages(a, it.b, it.seq.len, it.t0 * kTile);
+                for (int t = it.t0; t < it.t1 && ok; ++t) {
+                    const int row = pages.row_of(a, t * kTile + min(lane, boxes - 1) * rows, status);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = ok && mbar_wait(&empty[stage], phase ^ 1, abort_flag, status);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&full[stage], kStageBytes);
+                        __syncwarp();
+                        if (lane < boxes)
+                            tma_load_2d(smem + F::kRingOff + stage * kStageBytes + lane * rows * kDim,
+                                        kv == 0 ? &tmap_k : &tmap_v, &full[stage], it.hk * kDim, row);
+                        ++issued;
+                        if (++stage == F::kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+            }
+            // no copy may be in flight when the CTA leaves
+            const uint32_t from = issued > F::kStages ? issued - F::kStages : 0;
+            for (uint32_t i = from; i < issued; ++i)
+                mbar_wait(&full[i % F::kStages], (i / F::kStages) & 1, nullptr, status);
+        } else if (warp == 13 && lane == 0) {
+            // -------------------------------------------------------- MMA issuer
+            // MMAs of one thread run in the order they are issued, so the
+            // scores of the next tile may follow the product that still reads
+            // the weights in their place.
+            constexpr uint32_t id_s = umma_idesc_e4m3(kHalfRows, kTile);
+            constexpr uint32_t id_o = idesc_f16_b_mn(kHalfRows, kDim);
+            uint32_t kstage = 0, kphase = 0, vbuf = 0, vphase = 0;
+            uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0};
+            bool ok = true;
+            const uint32_t q_addr = smem_addr(smem), ring = smem_addr(smem + F::kRingOff),
+                           v16 = smem_addr(smem + F::kV16Off);
+            auto scores = [&](int half) {
+                tc_fence_after_sync();
+                const uint32_t k = ring + kstage * kStageBytes;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        umma_e4m3(tmem + F::s_col(half),
+                                  umma_desc_sw128(q_addr + (2 * half + part) * F::kQPart + 32 * s),
+                                  umma_desc_sw128(k + 32 * s), id_s, part + s > 0 ? 1u : 0u);
+                umma_commit(&sfull[half]);
+            };
+            auto next_k = [&] {
+                umma_commit(&empty[kstage]);
+                kstage += 2;
+                if (kstage == F::kStages) {
+                    kstage = 0;
+                    kphase ^= 1;
+                }
+            };
+            while (ok && it.next()) {
+                const int n = it.t1 - it.t0, count[2] = {it.count(0), it.count(1)};
+                ok = mbar_wait(&full[kstage], kphase, abort_flag, status);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (count[half] == 0) continue;
+                    ok = ok && mbar_wait(&qfull[half], qphase[half], abort_flag, status);
+                    qphase[half] ^= 1;
+                    if (ok) scores(half);
+                }
+                if (ok) next_k();
+                for (int j = 0; j < n && ok; ++j) {
+                    ok = mbar_wait(&vfull[vbuf], vphase, abort_flag, status);
+                    if (j + 1 < n) ok = ok && mbar_wait(&full[kstage], kphase, abort_flag, status);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (j >= count[half]) continue;
+                        ok = ok && mbar_wait(&pfull[half], pphase[half], abort_flag, status);
+                        if (!ok) break;
+                        pphase[half] ^= 1;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int s = 0; s < 8; ++s)  // 16 positions each
+                            umma_f16_ta(tmem + F::o_col(half), tmem + F::s_col(half) + 8 * s,
+                                        umma_desc_mn_sw128(v16 + vbuf * F::kV16 + 16 * 128 * s, F::kV16 / 2),
+                                        id_o, j + s > 0 ? 1u : 0u);
+                        if (j + 1 < count[half])
+                            scores(half);
+                        else
+                            umma_commit(&ofull[half]);
+                    }
+                    if (!ok) break;
+                    umma_commit(&vempty[vbuf]);
+                    if (j + 1 < n) next_k();
+                    vbuf ^= 1;
+                    vphase ^= vbuf ^ 1;
+                }
+            }
+        }
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+        // ------------------------------------------------------------ V to F16
+        const int row = threadIdx.x - 256;  // position in the tile
+        uint32_t stage = 1, phase = 0, vbuf = 0, vphase = 0;
+        bool ok = true;
+        while (ok && it.next()) {
+            for (int t = it.t0; t < it.t1 && ok; ++t) {
+                ok = mbar_wait(&full[stage], phase, abort_flag, status) &&
+                     mbar_wait(&vempty[vbuf], vphase ^ 1, abort_flag, status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint8_t *src = smem + F::kRingOff + stage * kStageBytes + row * kDim;
+                uint8_t *dst = smem + F::kV16Off + vbuf * F::kV16 + row * 128;
+                const int x = row & 7;
+                // what a page holds behind the sequence's end may be anything
+                const uint32_t keep = t * kTile + row < it.seq.len ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(src + ((c ^ x) << 4));
+                    const uint32_t w[4] = {u.x & keep, u.y & keep, u.z & keep, u.w & keep};
+                    uint32_t f[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        f[2 * k] = e4m3x2_to_f16_shifted(__byte_perm(w[k], 0, 0x1404));
+                        f[2 * k + 1] = e4m3x2_to_f16_shifted(__byte_perm(w[k], 0, 0x3424));
+                    }
+                    uint8_t *d = dst + (c >> 2) * (F::kV16 / 2);
+                    const int cc = (c & 3) * 2;
+                    *reinterpret_cast<uint4 *>(d + ((cc ^ x) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4 *>(d + (((cc + 1) ^ x) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&vfull[vbuf]);
+                    mbar_arrive(&empty[stage]);
+                }
+                stage += 2;
+                if (stage > F::kStages) {
+                    stage = 1;
+                    phase ^= 1;
+                }
+                vbuf ^= 1;
+                vphase ^= vbuf ^ 1;
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        // ------------------------------------------------------------ softmax
+        // A wait that gives up sets the abort flag: the loops then run to their
+        // end without waiting, so that every barrier still has all its warps.
+        const int half = warp >> 2, ht = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_tm = tmem + lanes + F::s_col(half), o_tm = tmem + lanes + F::o_col(half);
+        const int G = a.group;
+
+        // sequences without positions, and reports
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            if (threadIdx.x == 0 && seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
+            const Seq s = seq_of(a, b);
+            if (s.len > 0) continue;
+            const int64_t width = static_cast<int64_t>(a.q_heads) * kDim;
+            for (int64_t i = threadIdx.x; i < s.q_len * width; i += 256)
+                a.out[(s.q0 + i / width) * a.out_stride + i % width] = 0;
+            if (a.lse != nullptr)
+                for (int i = threadIdx.x; i < s.q_len * a.q_heads; i += 256)
+                    a.lse[static_cast<int64_t>(s.q0) * a.q_heads + i] = -INFINITY;
+        }
+
+        uint32_t sphase = 0, ophase = 0;
+        while (it.next()) {
+            if (half == 1 && !it.has_b()) continue;
+            const int n = it.count(half);
+            const int r = it.m * 256 + half * kHalfRows + ht;  // row of the sequence and head
+            const bool live = r < it.seq.q_len * G;
+            const int tok = r / G, head = it.hk * G + (r - tok * G);
+            const int64_t q_row = it.seq.q0 + tok;
+            float m_run = -INFINITY, l_run = 0.0f;
+            if (n > 0) {
+                // the row's query: power of two that takes its largest channel to
+                // [128, 256), two E4M3 parts, K-major with the 128-byte swizzle
+                uint4 u[16];
+                uint32_t top = 0;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + q_row * a.q_stride + static_cast<int64_t>(head) * kDim);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) u[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) top = max(top, amax_bits8(u[c]));
+                const int e = max(static_cast<int>(top >> 7) - 127, -100);
+                const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+                const float scale =
+                    a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+                uint8_t *dst = smem + 2 * half * F::kQPart + ht * kDim;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) {
+                        float f[8];
+                        unpack_bf16x8(u[2 * c + d], f);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float x0 = f[4 * k] * up, x1 = f[4 * k + 1] * up;
+                            const float x2 = f[4 * k + 2] * up, x3 = f[4 * k + 3] * up;
+                            const uint16_t h0 = e4m3x2_satfinite(x0, x1), h1 = e4m3x2_satfinite(x2, x3);
+                            const float2 d0 = e4m3x2_to_float2(h0), d1 = e4m3x2_to_float2(h1);
+                            hi[2 * d + k] = h0 | (static_cast<uint32_t>(h1) << 16);
+                            lo[2 * d + k] = e4m3x2_satfinite(x0 - d0.x, x1 - d0.y) |
+                                            (static_cast<uint32_t>(e4m3x2_satfinite(x2 - d1.x, x3 - d1.y)) << 16);
+                        }
+                    }
+                    const int off = (c ^ (ht & 7)) << 4;
+                    *reinterpret_cast<uint4 *>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(dst + F::kQPart + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&qfull[half]);
+
+                const int limit = live ? row_limit(a, it.seq, r) : -1;
+                for (int j = 0; j < n; ++j) {
+                    mbar_wait(&sfull[half], sphase, abort_flag, status);
+                    sphase ^= 1;
+                    tc_fence_after_sync();
+                    float v[128];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v + 32 * c);
+                    tmem_ld_wait<128>(v);
+                    const int seen = limit + 1 - (it.t0 + j) * kTile;  // columns the row sees
+                    if (__any_sync(0xFFFFFFFFu, seen < kTile)) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) v[c] = c < seen ? v[c] : -INFINITY;
+                    }
+                    float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int c = 4; c < 128; c += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mx[k] = fmaxf(mx[k], c + 4 + k < 128 ? fmaxf(v[c + k], v[c + 4 + k]) : v[c + k]);
+                    const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                    const bool move = z > m_run + kRescaleAt;  // always from -inf, if anything is seen
+                    if (__any_sync(0xFFFFFFFFu, move)) {
+                        const float f = move ? ex2(m_run - z) : 1.0f;
+                        if (move) m_run = z;
+                        l_run *= f;
+                        if (j > 0) {
+                            // the product that wrote O is complete: it was issued before these scores
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                float o[32];
+                                tmem_ld32(o_tm + 32 * c, o);
+                                tmem_ld_wait<32>(o);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= f;
+                                tmem_st32(o_tm + 32 * c, reinterpret_cast<const uint32_t *>(o));
+                            }
+                        }
+                    }
+                    const float neg = m_run == -INFINITY ? 0.0f : -m_run;
+                    const float2 s2 = make_float2(scale, scale), n2 = make_float2(neg, neg);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < 128; c += 64) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            float2 x = ffma2(make_float2(v[c + 2 * k], v[c + 2 * k + 1]), s2, n2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            sum[k & 1] = fadd2(sum[k & 1], x);
+                            p[k] = pack_f16(x.x, x.y);
+                        }
+                        tmem_st32(s_tm + c / 2, p);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[half]);
+                    sum[0] = fadd2(sum[0], sum[1]);
+                    l_run += sum[0].x + sum[0].y;
+                }
+                mbar_wait(&ofull[half], ophase, abort_flag, status);
+                ophase ^= 1;
+                tc_fence_after_sync();
+            }
+
+            // O times `f` (takes the 2^8 of V back), BF16
+            auto store_row = [&](float f, auto &&part) {
+                uint4 *out = reinterpret_cast<uint4 *>(a.out + q_row * a.out_stride + static_cast<int64_t>(head) * kDim);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    part(c, o);
+                    if (!live) continue;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float t[8];
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) t[d] = f != 0.0f ? o[8 * k + d] * f : 0.0f;
+                        out[4 * c + k] = pack_bf16x8(t);
+                    }
+                }
+            };
+            auto store_lse = [&](float m, float l) {
+                if (live && a.lse != nullptr)
+                    a.lse[q_row * a.q_heads + head] =
+                        l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            };
+            auto from_tmem = [&](int c, float *o) {
+                tmem_ld32(o_tm + 32 * c, o);
+                tmem_ld_wait<32>(o);
+            };
+            if (it.t0 == 0 && it.t1 == it.tiles) {
+                store_row(l_run > 0.0f ? __fdividef(256.0f, l_run) : 0.0f, from_tmem);
+                store_lse(m_run, l_run);
+                continue;
+            }
+            // partial: this CTA's slot 1 if the item begins here, else slot 0
+            const int64_t all = start_w[3], w_first = it.item(), w_last = w_first + it.tiles - 1;
+            auto owner = [&](int64_t w) { return static_cast<int>(((w + 1) * *parts - 1) / all); };
+            const int c_first = owner(w_first), c_last = owner(w_last);
+            auto slot = [&](int i) {
+                return partials + (static_cast<int64_t>(2 * i + (i == c_first ? 1 : 0)) * 2 + half) * F::kPartial;
+            };
+            float *mine = slot(blockIdx.x);
+            if (n > 0) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    from_tmem(c, o);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        __stcg(reinterpret_cast<float4 *>(mine) + (8 * c + k) * kHalfRows + ht,
+                               make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+                }
+            }
+            __stcg(mine + kHalfRows * kDim + ht, m_run);
+            __stcg(mine + kHalfRows * (kDim + 1) + ht, l_run);
+            __threadfence();
+            named_barrier(1 + half, 128);
+            if (ht == 0) {
+                const int seen = atomicAdd(counters + 2 * c_first + half, 1);
+                shared_last[half] = seen == c_last - c_first;
+                if (shared_last[half]) counters[2 * c_first + half] = 0;
+                __threadfence();
+            }
+            named_barrier(1 + half, 128);
+            if (!shared_last[half]) continue;
+            // join in the order of the CTAs, a row per thread
+            float m = -INFINITY, l = 0.0f;
+            for (int i = c_first; i <= c_last; ++i) m = fmaxf(m, __ldcg(slot(i) + kHalfRows * kDim + ht));
+            for (int i = c_first; i <= c_last && m > -INFINITY; ++i) {
+                const float *p = slot(i) + kHalfRows * kDim + ht;
+                l = fmaf(ex2(__ldcg(p) - m), __ldcg(p + kHalfRows), l);
+            }
+            store_row(l > 0.0f ? __fdividef(256.0f, l) : 0.0f, [&](int c, float *o) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+                if (l <= 0.0f) return;
+                for (int i = c_first; i <= c_last; ++i) {
+                    const float *p = slot(i);
+                    const float mi = __ldcg(p + kHalfRows * kDim + ht);
+                    if (mi == -INFINITY) continue;  // its O may never have been written
+                    const float f = ex2(mi - m);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p) + (8 * c + k) * kHalfRows + ht);
+                        o[4 * k] = fmaf(f, v.x, o[4 * k]);
+                        o[4 * k + 1] = fmaf(f, v.y, o[4 * k + 1]);
+                        o[4 * k + 2] = fmaf(f, v.z, o[4 * k + 2]);
+                        o[4 * k + 3] = fmaf(f, v.w, o[4 * k + 3]);
+                    }
+                }
+            });
+            store_lse(m, l);
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 13) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace attn
+}  // namespace fp8bq

@@ -25,7 +25,9 @@
 //                       smaller M: the decode GEMM, then silu_mul_quantize
 //   rms_norm_quantize -> rms_norm_kernel<V> (one CTA per row, V vectors per thread)
 //   rope_kv_write_e4m3 -> rope_kv_write_kernel
-//   paged_attention  -> attn::attention_simple_kernel
+//   paged_attention  -> up to 32 query rows (new tokens x heads of a group) per kv head:
+//                       attn::attention_few_kernel<8|16|32> (rows are the MMA's columns);
+//                       more: attn::attention_many_kernel (256 rows per CTA)
 //   linear           -> quantize_act into the workspace, then the gemm path; the
 //                       decode kernel then streams its first weight blocks while
 //                       the quantizer still runs (programmatic dependent launch)
@@ -43,6 +45,7 @@
 
 #include "attention.cuh"
 #include "attention_few.cuh"
+#include "attention_many.cuh"
 #include "fp8bq.h"
 #include "gemm_decode.cuh"
 #include "gemm_prefill.cuh"
@@ -249,7 +252,13 @@ const DeviceInfo *device_info() {
             cudaFuncSetAttribute(attn::attention_few_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  attn::Few<32>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(attn::attention_few_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 attn::Few<8>::kBytes) != cudaSuccess)
+                                 attn::Few<8>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(attn::attention_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 attn::Many::kBytes) != cudaSuccess)
+            return;
+        // the register split (setmaxnreg) assumes this launch allocation
+        if (cudaFuncGetAttributes(&fa, attn::attention_many_kernel) != cudaSuccess ||
+            fa.numRegs != attn::kManyLaunchRegs)
             return;
         for (int c = 2; c <= 8; ++c) {
             cudaLaunchConfig_t cfg = {};
@@ -718,6 +727,9 @@ int64_t attention_rows(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max
     return std::min(max_q_len, T) * (q_heads / kv_heads);
 }
 
+constexpr size_t kManyWsBytes = size_t(decode::kCounterBytes) +
+                                size_t(2 * 2) * attn::kManyMaxGrid * attn::Many::kPartial * 4;
+
 template <int NR>
 size_t few_ws_bytes() {
     return round256(decode::kCounterBytes + int64_t(2) * decode::kMaxGrid * attn::Few<NR>::kPartial * 4);
@@ -725,7 +737,7 @@ size_t few_ws_bytes() {
 
 size_t attention_ws_bytes(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_q_len) {
     const int64_t rows = attention_rows(T, q_heads, kv_heads, max_q_len);
-    return rows <= 8 ? few_ws_bytes<8>() : rows <= 16 ? few_ws_bytes<16>() : rows <= 32 ? few_ws_bytes<32>() : 0;
+    return rows <= 8 ? few_ws_bytes<8>() : rows <= 16 ? few_ws_bytes<16>() : rows <= 32 ? few_ws_bytes<32>() : kManyWsBytes;
 }
 
 template <int NR>
@@ -741,27 +753,28 @@ cudaError_t launch_few(const DeviceInfo &d, const attn::Args &a, const CUtensorM
 
 fp8bq_status launch_attention(const DeviceInfo &d, const attn::Args &a, int64_t num_slots, void *ws,
                               cudaStream_t st) {
+    // without a slot there is nothing to map: any descriptor will do, no page
+    // is in the cache
+    CUtensorMap tk, tv;
+    const uint32_t box = std::min<uint32_t>(1u << a.page_shift, attn::kTile);
+    const void *k = num_slots ? static_cast<const void *>(a.k_cache) : ws;
+    const void *v = num_slots ? static_cast<const void *>(a.v_cache) : ws;
+    const int64_t slots = std::max<int64_t>(num_slots, 1);
+    if (!make_tmap_2d(&tk, k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, slots, a.slot_stride, attn::kDim,
+                      box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
+        !make_tmap_2d(&tv, v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, slots, a.slot_stride, attn::kDim,
+                      box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
+        return FP8BQ_ERR_CUDA;
     const int64_t rows = int64_t(a.max_q) * a.group;
-    if (rows <= 32) {
-        // without a slot there is nothing to map: any descriptor will do, no
-        // page is in the cache
-        CUtensorMap tk, tv;
-        const uint32_t box = std::min<uint32_t>(1u << a.page_shift, attn::kTile);
-        const void *k = num_slots ? static_cast<const void *>(a.k_cache) : ws;
-        const void *v = num_slots ? static_cast<const void *>(a.v_cache) : ws;
-        const int64_t slots = std::max<int64_t>(num_slots, 1);
-        if (!make_tmap_2d(&tk, k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, slots, a.slot_stride, attn::kDim,
-                          box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
-            !make_tmap_2d(&tv, v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, slots, a.slot_stride, attn::kDim,
-                          box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
-            return FP8BQ_ERR_CUDA;
-        return from_cuda(rows <= 8    ? launch_few<8>(d, a, tk, tv, ws, st)
-                         : rows <= 16 ? launch_few<16>(d, a, tk, tv, ws, st)
-                                      : launch_few<32>(d, a, tk, tv, ws, st));
-    }
-    return from_cuda(launch(attn::attention_simple_kernel,
-                            dim3(static_cast<unsigned>(a.T * a.q_heads)),
-                            dim3(32 * attn::kSimpleWarps), 0, st, a, d.status));
+    if (rows <= 8) return from_cuda(launch_few<8>(d, a, tk, tv, ws, st));
+    if (rows <= 16) return from_cuda(launch_few<16>(d, a, tk, tv, ws, st));
+    if (rows <= 32) return from_cuda(launch_few<32>(d, a, tk, tv, ws, st));
+    const int grid = std::min<int>(d.sm_count, attn::kManyMaxGrid);
+    return from_cuda(launch(attn::attention_many_kernel, dim3(static_cast<unsigned>(grid)),
+                            dim3(attn::kManyThreads), attn::Many::kBytes, st, tk, tv, a,
+                            static_cast<int *>(ws),
+                            reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + decode::kCounterBytes),
+                            d.status));
 }
 
 }  // namespace
