@@ -26,8 +26,10 @@
 // nor a last wave leave SMs idle.  An item that lies in several CTAs is joined
 // as in attention_few.cuh, each half by itself.
 //
-// Roles (512 threads): warpgroups 0 and 1 softmax of A and B (192 registers a
-// thread: 128 scores), 2 converts V, warp 12 TMA producer, warp 13 MMA issuer.
+// Roles (512 threads): warpgroups 0 and 1 softmax of A and B (184 registers a
+// thread: 128 scores), 2 converts V, warp 12 TMA producer, warp 13 MMA issuer,
+// warp 14 walks the work list and publishes the segments to the others (which
+// have no registers to spare for it: walking it in every role spilled scores).
 #pragma once
 
 #include "attention_few.cuh"
@@ -37,7 +39,7 @@ namespace attn {
 
 constexpr int kManyThreads = 512;
 constexpr int kManyLaunchRegs = 128;
-constexpr int kSoftmaxRegs = 192, kConvertRegs = 72, kIssueRegs = 56;
+constexpr int kSoftmaxRegs = 184, kConvertRegs = 56, kIssueRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <=
                   kManyThreads * kManyLaunchRegs,
               "register split exceeds the launch allocation");
@@ -53,9 +55,11 @@ struct Many {
     static constexpr int kV16 = kTile * kDim * 2;     // 32 KB
     static constexpr int kV16Off = kRingOff + kStages * kStageBytes;
     static constexpr int kBarOff = kV16Off + 2 * kV16;
-    // full, empty; vfull, vempty, qfull, sfull, pfull, ofull (two each)
-    static constexpr int kBars = 2 * kStages + 12;
-    static constexpr int kMiscOff = kBarOff + kBars * 8;
+    static constexpr int kSegs = 4;  // published segments
+    // full, empty; vfull, vempty, qfull, sfull, pfull, ofull (two each); segfull, segempty
+    static constexpr int kBars = 2 * kStages + 12 + 2 * kSegs;
+    static constexpr int kSegOff = kBarOff + kBars * 8;
+    static constexpr int kMiscOff = kSegOff + kSegs * 64;
     static constexpr int kBytes = kMiscOff + 256 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory");
     // floats of one half's partial: O [32 groups of 4 channels][128 rows][4], max, sum [128]
@@ -114,6 +118,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
         "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
         "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
         "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
 
@@ -177,12 +190,10 @@ struct Items {
     int cost;                // positions of one head's item of block m
     // the current segment
     int hk, t0, t1;          // kv head, tiles [t0, t1)
-    int tiles, tiles_a;      // of the whole item; of its half A
-    int rows;                // of the item, 1 .. 256
 
     __device__ Items(const Args &args, int64_t w0, int64_t w1, int b0, int m0, int64_t base0)
         : a(args), w(w0), w_end(w1), base(base0), b(b0), m(m0), blocks(0), cost(0), hk(0), t0(0),
-          t1(0), tiles(0), tiles_a(0), rows(0) {
+          t1(0) {
         if (w < w_end) {
             seq = seq_of(a, b);
             blocks = row_blocks(a, seq);
@@ -209,20 +220,47 @@ struct Items {
             t0 = max(rel - kItemCost, 0);
             t1 = max(static_cast<int>(rel + left) - kItemCost, 0);
             w += left;
-            if (t1 > t0) break;
+            if (t1 > t0) return true;
         }
-        tiles = cost - kItemCost;
-        tiles_a = tiles_until(a, seq, m * 256 + 128);
-        rows = min(seq.q_len * a.group - m * 256, 256);
-        return true;
-    }
-    __device__ bool has_b() const { return rows > kHalfRows; }
-    // tiles of a half in this segment
-    __device__ int count(int half) const {
-        return half == 0 ? max(min(t1, tiles_a) - t0, 0) : has_b() ? t1 - t0 : 0;
     }
     __device__ int64_t item() const { return base + static_cast<int64_t>(hk) * cost + kItemCost; }
 };
+
+// A segment as its users read it (shared memory).
+struct Segment {
+    int valid;           // 0: the CTA's part is done
+    int b, hk, t0, t1;   // sequence, kv head, tiles
+    int count[2];        // tiles of each half, from t0 on
+    int has_b;           // the item has rows in half B
+    int row0, rows_end;  // first row of half A; rows of the sequence and head
+    int len, q0;         // positions; first row of q
+    int limit0;          // last position that row 0 sees (may be negative); one more per token
+    int whole;           // all tiles of the item: no partial
+    int c_first, c_last; // CTAs that have tiles of the item
+};
+static_assert(sizeof(Segment) == 64, "shared-memory layout");
+
+// Reads the published segments in order; every lane of a using warp keeps one.
+struct SegReader {
+    uint64_t *full, *empty;
+    const Segment *ring;
+    uint32_t i, phase;
+
+    __device__ const Segment *next(volatile int *abort_flag, int *status) const {
+        if (!mbar_wait(&full[i], phase, abort_flag, status)) return nullptr;
+        return ring[i].valid ? ring + i : nullptr;
+    }
+    // Warp-wide: this warp is done with the current one.
+    __device__ void release() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[i]);
+        if (++i == Many::kSegs) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+};
+constexpr int kSegUsers = 14;  // warps: producer, MMA, 4 converting, 8 softmax
 
 // ------------------------------------------------------------------ kernel
 
@@ -237,7 +275,9 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + F::kBarOff);
     uint64_t *empty = full + F::kStages;
     uint64_t *vfull = empty + F::kStages, *vempty = vfull + 2, *qfull = vempty + 2,
-             *sfull = qfull + 2, *pfull = sfull + 2, *ofull = pfull + 2;
+             *sfull = qfull + 2, *pfull = sfull + 2, *ofull = pfull + 2, *segfull = ofull + 2,
+             *segempty = segfull + F::kSegs;
+    Segment *seg_ring = reinterpret_cast<Segment *>(smem + F::kSegOff);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + F::kMiscOff);
     uint32_t *tmem_slot = misc;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
@@ -261,6 +301,10 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i], 4);
             mbar_init(&ofull[i], 1);
+        }
+        for (int i = 0; i < F::kSegs; ++i) {
+            mbar_init(&segfull[i], 1);
+            mbar_init(&segempty[i], kSegUsers);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -334,7 +378,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    Items it(a, start_w[0], start_w[1], start_bm[0], start_bm[1], start_w[2]);
+    SegReader segs{segfull, segempty, seg_ring, 0, 0};
 
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
@@ -343,9 +387,12 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int rows = min(1 << a.page_shift, kTile), boxes = kTile / rows;
             uint32_t stage = 0, phase = 0, issued = 0;
             bool ok = true;
-            while (ok && it.next()) {
-                PageWalk pages(a, it.b, it.seq.len, it.t0 * kTile);
-                for (int t = it.t0; t < it.t1 && ok; ++t) {
+            while (ok) {
+                const Segment *sg = segs.next(abort_flag, status);
+                if (!__all_sync(0xFFFFFFFFu, sg != nullptr)) break;
+                const int hk = sg->hk, t1 = sg->t1;
+                PageWalk pages(a, sg->b, sg->len, sg->t0 * kTile);
+                for (int t = sg->t0; t < t1 && ok; ++t) {
                     const int row = pages.row_of(a, t * kTile + min(lane, boxes - 1) * rows, status);
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
@@ -356,7 +403,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         __syncwarp();
                         if (lane < boxes)
                             tma_load_2d(smem + F::kRingOff + stage * kStageBytes + lane * rows * kDim,
-                                        kv == 0 ? &tmap_k : &tmap_v, &full[stage], it.hk * kDim, row);
+                                        kv == 0 ? &tmap_k : &tmap_v, &full[stage], hk * kDim, row);
                         ++issued;
                         if (++stage == F::kStages) {
                             stage = 0;
@@ -364,12 +411,50 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         }
                     }
                 }
+                segs.release();
             }
             // no copy may be in flight when the CTA leaves
             const uint32_t from = issued > F::kStages ? issued - F::kStages : 0;
             for (uint32_t i = from; i < issued; ++i)
                 mbar_wait(&full[i % F::kStages], (i / F::kStages) & 1, nullptr, status);
-        } else if (warp == 13 && lane == 0) {
+        } else if (warp == 14) {
+            // -------------------------------------------------------- work list
+            if (lane == 0) {
+                Items it(a, start_w[0], start_w[1], start_bm[0], start_bm[1], start_w[2]);
+                const int64_t all = start_w[3], np = *parts;
+                uint32_t i = 0, phase = 0;
+                for (bool more = true; more;) {
+                    more = it.next();
+                    if (!mbar_wait(&segempty[i], phase ^ 1, abort_flag, status)) break;
+                    Segment &sg = seg_ring[i];
+                    sg.valid = more;
+                    if (more) {
+                        sg.b = it.b;
+                        sg.hk = it.hk;
+                        sg.t0 = it.t0;
+                        sg.t1 = it.t1;
+                        const int last_row = min(it.m * 256 + 256, it.seq.q_len * a.group);
+                        sg.has_b = last_row > it.m * 256 + kHalfRows;
+                        sg.count[0] = max(min(it.t1, tiles_until(a, it.seq, it.m * 256 + kHalfRows)) - it.t0, 0);
+                        sg.count[1] = sg.has_b ? it.t1 - it.t0 : 0;
+                        sg.row0 = it.m * 256;
+                        sg.rows_end = it.seq.q_len * a.group;
+                        sg.len = it.seq.len;
+                        sg.q0 = it.seq.q0;
+                        sg.limit0 = it.seq.len - it.seq.q_real;
+                        sg.whole = it.t0 == 0 && it.t1 == it.cost - kItemCost;
+                        const int64_t w0 = it.item(), w1 = w0 + it.cost - kItemCost - 1;
+                        sg.c_first = static_cast<int>(((w0 + 1) * np - 1) / all);
+                        sg.c_last = static_cast<int>(((w1 + 1) * np - 1) / all);
+                    }
+                    mbar_arrive(&segfull[i]);
+                    if (++i == F::kSegs) {
+                        i = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        } else if (warp == 13) {
             // -------------------------------------------------------- MMA issuer
             // MMAs of one thread run in the order they are issued, so the
             // scores of the next tile may follow the product that still reads
@@ -401,8 +486,15 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     kphase ^= 1;
                 }
             };
-            while (ok && it.next()) {
-                const int n = it.t1 - it.t0, count[2] = {it.count(0), it.count(1)};
+            while (ok && lane == 0) {
+                const Segment *sg = segs.next(abort_flag, status);
+                if (sg == nullptr) break;
+                const int n = sg->t1 - sg->t0, count[2] = {sg->count[0], sg->count[1]};
+                mbar_arrive(&segempty[segs.i]);
+                if (++segs.i == F::kSegs) {
+                    segs.i = 0;
+                    segs.phase ^= 1;
+                }
                 ok = mbar_wait(&full[kstage], kphase, abort_flag, status);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -446,8 +538,13 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const int row = threadIdx.x - 256;  // position in the tile
         uint32_t stage = 1, phase = 0, vbuf = 0, vphase = 0;
         bool ok = true;
-        while (ok && it.next()) {
-            for (int t = it.t0; t < it.t1 && ok; ++t) {
+        while (ok) {
+            const Segment *sg = segs.next(abort_flag, status);
+            if (!__all_sync(0xFFFFFFFFu, sg != nullptr)) break;
+            const int t1 = sg->t1, len = sg->len;
+            int t = sg->t0;
+            segs.release();
+            for (; t < t1 && ok; ++t) {
                 ok = mbar_wait(&full[stage], phase, abort_flag, status) &&
                      mbar_wait(&vempty[vbuf], vphase ^ 1, abort_flag, status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
@@ -456,8 +553,8 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 uint8_t *dst = smem + F::kV16Off + vbuf * F::kV16 + row * 128;
                 const int x = row & 7;
                 // what a page holds behind the sequence's end may be anything
-                const uint32_t keep = t * kTile + row < it.seq.len ? 0xFFFFFFFFu : 0u;
-#pragma unroll
+                const uint32_t keep = t * kTile + row < len ? 0xFFFFFFFFu : 0u;
+#pragma unroll 4
                 for (int c = 0; c < 8; ++c) {
                     const uint4 u = *reinterpret_cast<const uint4 *>(src + ((c ^ x) << 4));
                     const uint32_t w[4] = {u.x & keep, u.y & keep, u.z & keep, u.w & keep};
@@ -511,13 +608,15 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
 
         uint32_t sphase = 0, ophase = 0;
-        while (it.next()) {
-            if (half == 1 && !it.has_b()) continue;
-            const int n = it.count(half);
-            const int r = it.m * 256 + half * kHalfRows + ht;  // row of the sequence and head
-            const bool live = r < it.seq.q_len * G;
-            const int tok = r / G, head = it.hk * G + (r - tok * G);
-            const int64_t q_row = it.seq.q0 + tok;
+        for (;; segs.release()) {
+            const Segment *sg = segs.next(abort_flag, status);
+            if (sg == nullptr) break;
+            if (half == 1 && !sg->has_b) continue;
+            const int n = sg->count[half];
+            const int r = sg->row0 + half * kHalfRows + ht;  // row of the sequence and head
+            const bool live = r < sg->rows_end;
+            const int tok = r / G, head = sg->hk * G + (r - tok * G);
+            const int64_t q_row = sg->q0 + tok;
             float m_run = -INFINITY, l_run = 0.0f;
             if (n > 0) {
                 // the row's query: power of two that takes its largest channel to
@@ -561,8 +660,10 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&qfull[half]);
 
-                const int limit = live ? row_limit(a, it.seq, r) : -1;
-                for (int j = 0; j < n; ++j) {
+                // columns of tile t0 that the row sees, 128 fewer per tile
+                int seen = (live ? (a.causal ? min(sg->limit0 + tok, sg->len - 1) : sg->len - 1) : -1) + 1 -
+                           sg->t0 * kTile;
+                for (int j = 0; j < n; ++j, seen -= kTile) {
                     mbar_wait(&sfull[half], sphase, abort_flag, status);
                     sphase ^= 1;
                     tc_fence_after_sync();
@@ -570,7 +671,6 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v + 32 * c);
                     tmem_ld_wait<128>(v);
-                    const int seen = limit + 1 - (it.t0 + j) * kTile;  // columns the row sees
                     if (__any_sync(0xFFFFFFFFu, seen < kTile)) {
 #pragma unroll
                         for (int c = 0; c < 128; ++c) v[c] = c < seen ? v[c] : -INFINITY;
@@ -589,14 +689,14 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         l_run *= f;
                         if (j > 0) {
                             // the product that wrote O is complete: it was issued before these scores
+#pragma unroll 1
+                            for (int c = 0; c < 128; c += 16) {
+                                float o[16];
+                                tmem_ld<16>(o_tm + c, o);
+                                tmem_ld_wait<16>(o);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                float o[32];
-                                tmem_ld32(o_tm + 32 * c, o);
-                                tmem_ld_wait<32>(o);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= f;
-                                tmem_st32(o_tm + 32 * c, reinterpret_cast<const uint32_t *>(o));
+                                for (int k = 0; k < 16; ++k) o[k] *= f;
+                                tmem_st16(o_tm + c, reinterpret_cast<const uint32_t *>(o));
                             }
                         }
                     }
@@ -654,15 +754,13 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 tmem_ld32(o_tm + 32 * c, o);
                 tmem_ld_wait<32>(o);
             };
-            if (it.t0 == 0 && it.t1 == it.tiles) {
+            if (sg->whole) {
                 store_row(l_run > 0.0f ? __fdividef(256.0f, l_run) : 0.0f, from_tmem);
                 store_lse(m_run, l_run);
                 continue;
             }
             // partial: this CTA's slot 1 if the item begins here, else slot 0
-            const int64_t all = start_w[3], w_first = it.item(), w_last = w_first + it.tiles - 1;
-            auto owner = [&](int64_t w) { return static_cast<int>(((w + 1) * *parts - 1) / all); };
-            const int c_first = owner(w_first), c_last = owner(w_last);
+            const int c_first = sg->c_first, c_last = sg->c_last;
             auto slot = [&](int i) {
                 return partials + (static_cast<int64_t>(2 * i + (i == c_first ? 1 : 0)) * 2 + half) * F::kPartial;
             };
