@@ -399,61 +399,84 @@ def nvfp4_gemm_a16(x: torch.Tensor, packed: torch.Tensor, sb: torch.Tensor, g: t
 
 
 # The calls below take several tensors of one device, which need not be the
-# current one: each is checked and the library is called with that device current.
-def _rows(t: torch.Tensor, cols: int, name: str, like: torch.Tensor) -> None:
-    """t: BF16 [rows of like, cols] with unit column stride (rows may be strided)."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != like.shape[0] or t.shape[1] != cols:
-        raise ValueError(f"{name} must be BF16 [{like.shape[0]}, {cols}], got {tuple(t.shape)}")
-    if t.shape[0] > 1 and t.shape[1] > 1 and t.stride(1) != 1:
+# current one.  A check that passes costs one expression (a few hundred
+# nanoseconds) and gives the pointer; _refuse finds what is wrong otherwise.
+def _refuse(t, dtype, shape, dev, name) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous (row-major)")
+
+
+def _dense(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int, name: str) -> int:
+    """The pointer of a contiguous tensor of this type and shape on this device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, shape, dev, name)
+
+
+def _rows(t: torch.Tensor, cols: int, rows: int, dev: int, name: str) -> tuple[int, int]:
+    """Pointer and row stride of a BF16 [rows, cols] tensor with unit column stride."""
+    if t.dtype is torch.bfloat16 and t.shape == (rows, cols) and t.get_device() == dev:
+        step, unit = t.stride()
+        if rows > 1 and unit == 1:
+            return t.data_ptr(), step
+        if rows <= 1 and (unit == 1 or cols <= 1):
+            return t.data_ptr(), max(step, cols)
         raise ValueError(f"{name} must have unit column stride")
-    _on(t, name, like)
+    _refuse(t, torch.bfloat16, (rows, cols), dev, name)
 
 
-def _on(t: torch.Tensor, name: str, like: torch.Tensor) -> None:
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+def _first(t: torch.Tensor, name: str) -> int:
+    """The device of a call, from its first tensor: BF16, two dimensions."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    return t.get_device()
 
 
-def _dense(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, like: torch.Tensor) -> None:
-    _need(t, dtype, name)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    _on(t, name, like)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _call(t: torch.Tensor, name: str, *args) -> None:
+def _call(t: torch.Tensor, dev: int, name: str, *args) -> None:
     """Calls the library on t's device and its current stream (passed as the last argument)."""
     f = getattr(lib(), name)
-    if t.get_device() == torch.cuda.current_device():
-        _check(f(*args, _stream(t)), name)
+    if dev == _get_device():
+        status = f(*args, _stream(t))
     else:
-        with torch.cuda.device(t.device):
-            _check(f(*args, _stream(t)), name)
+        with torch.cuda.device(dev):
+            status = f(*args, _stream(t))
+    if status != 0:
+        raise Fp8bqError(status, name)
 
 
 def _norm(x, weight, eps, residual, residual_out, q, s, h) -> None:
-    _need(x, torch.bfloat16, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be BF16 [M, K]")
-    M, K = x.shape
-    _dense(weight, torch.bfloat16, (K,), "weight", x)
+    dev = _first(x, "x")
+    shape = x.shape
+    M, K = shape
+    px = _dense(x, torch.bfloat16, shape, dev, "x")
+    pw = _dense(weight, torch.bfloat16, (K,), dev, "weight")
+    pr = po = None
     if residual is not None:
-        _dense(residual, torch.bfloat16, (M, K), "residual", x)
-        if residual_out is None:
-            residual_out = residual
-        _dense(residual_out, torch.bfloat16, (M, K), "residual_out", x)
+        pr = po = _dense(residual, torch.bfloat16, shape, dev, "residual")
+        if residual_out is not None:
+            po = _dense(residual_out, torch.bfloat16, shape, dev, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if h is not None:
-        _dense(h, torch.bfloat16, (M, K), "h", x)
-    _call(x, "fp8bq_rms_norm_quantize", _ptr(x), _ptr(residual), _ptr(weight), eps, M, K,
-          _ptr(residual_out), _ptr(q), _ptr(s), _ptr(h))
+    pq = ps = None
+    if q is not None:
+        pq = _dense(_codes(q), torch.uint8, shape, dev, "q")
+        ps = _dense(s, torch.float32, (M, K // 128), dev, "s")
+    ph = None if h is None else _dense(h, torch.bfloat16, shape, dev, "h")
+    _call(x, dev, "fp8bq_rms_norm_quantize", px, pr, pw, eps, M, K, po, pq, ps, ph)
 
 
 def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
@@ -465,17 +488,13 @@ def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
     r = BF16(x + residual) -> (codes uint8 [M, K], scales FP32 [M, K/128]).  x, residual: BF16
     [M, K]; weight: BF16 [K].  r goes to residual_out, or in place of residual when that is
     not given.  Pass h (BF16 [M, K]) to also receive the norm itself."""
-    _need(x, torch.bfloat16, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be BF16 [M, K]")
-    M, K = x.shape
-    if q is None:
-        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    if s is None:
-        s = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
-    q = _codes(q)
-    _dense(q, torch.uint8, (M, K), "q", x)
-    _dense(s, torch.float32, (M, K // 128), "s", x)
+    if q is None or s is None:
+        _first(x, "x")
+        M, K = x.shape
+        if q is None:
+            q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        if s is None:
+            s = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
     _norm(x, weight, eps, residual, residual_out, q, s, h)
     return q, s
 
@@ -506,13 +525,13 @@ def rope_inv_freq(rot_dim: int, base: float, scaling: str = "plain", factor: flo
     return (f if device is None else f.to(device)), m.value
 
 
-def _caches(k_cache, v_cache, like):
-    k_cache, v_cache = _codes(k_cache), _codes(v_cache)
-    if k_cache.dim() != 2:
+def _caches(k_cache, v_cache, dev) -> tuple[int, int, int, int]:
+    """Pointers, slots and slot bytes of the two E4M3 caches."""
+    shape = k_cache.shape
+    if len(shape) != 2:
         raise ValueError("k_cache and v_cache must be [num_slots, slot_bytes]")
-    _dense(k_cache, torch.uint8, tuple(k_cache.shape), "k_cache", like)
-    _dense(v_cache, torch.uint8, tuple(k_cache.shape), "v_cache", like)
-    return k_cache, v_cache
+    return (_dense(_codes(k_cache), torch.uint8, shape, dev, "k_cache"),
+            _dense(_codes(v_cache), torch.uint8, shape, dev, "v_cache"), shape[0], shape[1])
 
 
 def rope_kv_write_e4m3(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -526,30 +545,28 @@ def rope_kv_write_e4m3(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: tor
     float8_e4m3fn [num_slots, slot_bytes]).  kv_heads defaults to slot_bytes / head_dim.
     Returns the rotated queries q_out (BF16 [T, q_heads head_dim], new unless given; may be
     qkv's own query columns)."""
-    if not qkv.is_cuda or qkv.dim() != 2:
-        raise ValueError("qkv must be a 2-D CUDA tensor")
-    _rows(qkv, qkv.shape[1], "qkv", qkv)
+    dev = _first(qkv, "qkv")
     T, cols = qkv.shape
-    k_cache, v_cache = _caches(k_cache, v_cache, qkv)
+    px, step = _rows(qkv, cols, T, dev, "qkv")
+    pk, pv, slots, slot_bytes = _caches(k_cache, v_cache, dev)
     if head_dim <= 0 or cols % head_dim:
         raise ValueError("qkv columns must be a multiple of head_dim")
     if kv_heads is None:
-        kv_heads = k_cache.shape[1] // head_dim
+        kv_heads = slot_bytes // head_dim
     q_heads = cols // head_dim - 2 * kv_heads
     if q_heads <= 0:
         raise ValueError(f"qkv of {cols} columns has no query heads beside 2 x {kv_heads} kv heads")
-    _dense(positions, torch.int64, (T,), "positions", qkv)
-    _dense(loc, torch.int64, (T,), "loc", qkv)
+    pp = _dense(positions, torch.int64, (T,), dev, "positions")
+    pl = _dense(loc, torch.int64, (T,), dev, "loc")
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be FP32 [rot_dim / 2]")
-    _dense(inv_freq, torch.float32, tuple(inv_freq.shape), "inv_freq", qkv)
+    pairs = inv_freq.shape[0]
+    pf = _dense(inv_freq, torch.float32, (pairs,), dev, "inv_freq")
     if q_out is None:
         q_out = torch.empty((T, q_heads * head_dim), dtype=torch.bfloat16, device=qkv.device)
-    _rows(q_out, q_heads * head_dim, "q_out", qkv)
-    _call(qkv, "fp8bq_rope_kv_write_e4m3", _ptr(qkv), _row_stride(qkv), T, q_heads, kv_heads,
-          head_dim, _ptr(positions), _ptr(inv_freq), 2 * inv_freq.numel(), int(interleaved), mscale,
-          _ptr(loc), _ptr(q_out), _row_stride(q_out), _ptr(k_cache),
-          _ptr(v_cache), k_cache.shape[0], k_cache.shape[1])
+    po, out_step = _rows(q_out, q_heads * head_dim, T, dev, "q_out")
+    _call(qkv, dev, "fp8bq_rope_kv_write_e4m3", px, step, T, q_heads, kv_heads, head_dim, pp, pf,
+          2 * pairs, 1 if interleaved else 0, mscale, pl, po, out_step, pk, pv, slots, slot_bytes)
     return q_out
 
 
@@ -577,33 +594,29 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     may be strided); seq_lens int32 [B], cu_q int32 [B + 1].  scale defaults to 128^-1/2.  Pass
     lse (FP32 [T, q_heads]) to also receive the log of the softmax's denominator.  Out-of-range
     pages and lengths are reported through last_device_status()."""
-    if not q.is_cuda or q.dim() != 2:
-        raise ValueError("q must be a 2-D CUDA tensor")
-    _rows(q, q_heads * HEAD_DIM, "q", q)
-    T = q.shape[0]
-    k_cache, v_cache = _caches(k_cache, v_cache, q)
-    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+    dev = _first(q, "q")
+    T, width = q.shape[0], q_heads * HEAD_DIM
+    pq, step = _rows(q, width, T, dev, "q")
+    pk, pv, slots, slot_bytes = _caches(k_cache, v_cache, dev)
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2:
         raise TypeError("page_table must be int32 [B, max_pages]")
-    _on(page_table, "page_table", q)
+    if page_table.get_device() != dev:
+        raise ValueError(f"page_table must be on cuda:{dev}, got {page_table.device}")
     B, pages = page_table.shape
-    if B > 0 and pages > 1 and page_table.stride(1) != 1:
+    table_step, unit = page_table.stride()
+    if pages > 1 and unit != 1 and B > 0:
         raise ValueError("page_table must have unit column stride")
-    _dense(seq_lens, torch.int32, (B,), "seq_lens", q)
-    _dense(cu_q, torch.int32, (B + 1,), "cu_q", q)
+    pl = _dense(seq_lens, torch.int32, (B,), dev, "seq_lens")
+    pc = _dense(cu_q, torch.int32, (B + 1,), dev, "cu_q")
     if out is None:
-        out = torch.empty((T, q_heads * HEAD_DIM), dtype=torch.bfloat16, device=q.device)
-    _rows(out, q_heads * HEAD_DIM, "out", q)
-    if lse is not None:
-        _dense(lse, torch.float32, (T, q_heads), "lse", q)
+        out = torch.empty((T, width), dtype=torch.bfloat16, device=q.device)
+    po, out_step = _rows(out, width, T, dev, "out")
+    pe = None if lse is None else _dense(lse, torch.float32, (T, q_heads), dev, "lse")
     if workspace is None:
         workspace = new_attention_workspace(T, B, q_heads, kv_heads, max_q_len, q.device)
-    _on(workspace, "workspace", q)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _call(q, "fp8bq_paged_attention", _ptr(q), _row_stride(q), _ptr(k_cache), _ptr(v_cache),
-          k_cache.shape[0], k_cache.shape[1], _ptr(page_table),
-          page_table.stride(0) if B > 1 else max(pages, page_table.stride(0)), pages, page_size,
-          _ptr(seq_lens), _ptr(cu_q), B, T, q_heads, kv_heads, max_q_len,
-          HEAD_DIM ** -0.5 if scale is None else scale, int(causal), _ptr(out), _row_stride(out),
-          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size())
+    pw = _dense(workspace, torch.uint8, workspace.shape, dev, "workspace")
+    _call(q, dev, "fp8bq_paged_attention", pq, step, pk, pv, slots, slot_bytes,
+          page_table.data_ptr(), table_step if B > 1 else max(pages, table_step), pages, page_size,
+          pl, pc, B, T, q_heads, kv_heads, max_q_len, HEAD_DIM ** -0.5 if scale is None else scale,
+          1 if causal else 0, po, out_step, pe, pw, workspace.numel())
     return out

@@ -573,12 +573,13 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (st == 0 && seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
             const Seq s = seq_of(a, b);
             if (s.len > 0) continue;
-            const int64_t width = static_cast<int64_t>(a.q_heads) * kDim;
-            for (int64_t i = st; i < s.q_len * width; i += kThreads)
-                a.out[(s.q0 + i / width) * a.out_stride + i % width] = 0;
-            if (a.lse != nullptr)
-                for (int i = st; i < s.q_len * a.q_heads; i += kThreads)
-                    a.lse[static_cast<int64_t>(s.q0) * a.q_heads + i] = -INFINITY;
+            for (int i = 0; i < s.q_len; ++i) {
+                const int64_t row = s.q0 + i;
+                uint4 *o = reinterpret_cast<uint4 *>(a.out + row * a.out_stride);
+                for (int c = st; c < a.q_heads * (kDim / 8); c += kThreads) o[c] = make_uint4(0, 0, 0, 0);
+                if (a.lse != nullptr)
+                    for (int h = st; h < a.q_heads; h += kThreads) a.lse[row * a.q_heads + h] = -INFINITY;
+            }
         }
 
         float l_run[NR];     // sums over this thread's positions

@@ -20,6 +20,9 @@
 // moved when a row's scores pass it by 2^8 (weights up to 2^8 are as exact in
 // F16 and FP32), so O is hardly ever rescaled in the tensor memory.
 //
+// Blocks of at most 128 rows have no second half: there both halves hold the same
+// rows and take the tiles in turn, and are joined like two CTAs.
+//
 // Work is a list of K/V tiles ordered by (sequence, 256 rows, kv head, tile),
 // each (rows, head) item preceded by kItemCost tiles' worth of nothing; CTA c of
 // one per SM takes the c-th equal part, so that neither causal masks nor lengths
@@ -56,8 +59,8 @@ struct Many {
     static constexpr int kV16Off = kRingOff + kStages * kStageBytes;
     static constexpr int kBarOff = kV16Off + 2 * kV16;
     static constexpr int kSegs = 4;  // published segments
-    // full, empty; vfull, vempty, qfull, sfull, pfull, ofull (two each); segfull, segempty
-    static constexpr int kBars = 2 * kStages + 12 + 2 * kSegs;
+    // full, empty; vfull, vempty, qfull, sfull, ofull (two each), pfull (four); segfull, segempty
+    static constexpr int kBars = 2 * kStages + 14 + 2 * kSegs;
     static constexpr int kSegOff = kBarOff + kBars * 8;
     static constexpr int kMiscOff = kSegOff + kSegs * 64;
     static constexpr int kBytes = kMiscOff + 256 + 1024;
@@ -160,13 +163,13 @@ __device__ __forceinline__ int row_limit(const Args &a, const Seq &s, int r) {
     return a.causal ? min(s.len - s.q_real + r / a.group, s.len - 1) : s.len - 1;
 }
 
-// 256-row blocks of a sequence with positions.
+// 256-row blocks of a sequence.
 __device__ __forceinline__ int row_blocks(const Args &a, const Seq &s) {
-    return s.len > 0 ? (s.q_len * a.group + 255) / 256 : 0;
+    return (s.q_len * a.group + 255) / 256;
 }
 
-// K/V tiles that rows [.., end) of a sequence need (at least one, which then
-// masks everything).
+// K/V tiles that rows [.., end) of a sequence need: at least one, which then
+// masks everything and makes the zeros of rows that see nothing.
 __device__ __forceinline__ int tiles_until(const Args &a, const Seq &s, int end) {
     return max(row_limit(a, s, min(end, s.q_len * a.group) - 1) / kTile + 1, 1);
 }
@@ -231,7 +234,7 @@ struct Segment {
     int valid;           // 0: the CTA's part is done
     int b, hk, t0, t1;   // sequence, kv head, tiles
     int count[2];        // tiles of each half, from t0 on
-    int has_b;           // the item has rows in half B
+    int dual;            // at most 128 rows: the halves hold the same and take tiles in turn
     int row0, rows_end;  // first row of half A; rows of the sequence and head
     int len, q0;         // positions; first row of q
     int limit0;          // last position that row 0 sees (may be negative); one more per token
@@ -275,15 +278,15 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + F::kBarOff);
     uint64_t *empty = full + F::kStages;
     uint64_t *vfull = empty + F::kStages, *vempty = vfull + 2, *qfull = vempty + 2,
-             *sfull = qfull + 2, *pfull = sfull + 2, *ofull = pfull + 2, *segfull = ofull + 2,
+             *sfull = qfull + 2, *ofull = sfull + 2, *pfull = ofull + 2, *segfull = pfull + 4,
              *segempty = segfull + F::kSegs;
     Segment *seg_ring = reinterpret_cast<Segment *>(smem + F::kSegOff);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + F::kMiscOff);
     uint32_t *tmem_slot = misc;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
-    int *shared_last = reinterpret_cast<int *>(misc + 2);      // [2]
-    int *start_bm = reinterpret_cast<int *>(misc + 4);         // sequence, block
-    int *parts = reinterpret_cast<int *>(misc + 6);            // CTAs that have a part
+    int *shared_last = reinterpret_cast<int *>(misc + 2);      // of half A, half B, doubled halves
+    int *start_bm = reinterpret_cast<int *>(misc + 5);         // sequence, block
+    int *parts = reinterpret_cast<int *>(misc + 7);            // CTAs that have a part
     int64_t *start_w = reinterpret_cast<int64_t *>(misc + 8);  // w0, w1, base, total
     int64_t *warp_cost = start_w + 4;                          // [16]
 
@@ -299,9 +302,9 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(&vempty[i], 1);
             mbar_init(&qfull[i], 4);
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 4);
             mbar_init(&ofull[i], 1);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&pfull[i], 4);
         for (int i = 0; i < F::kSegs; ++i) {
             mbar_init(&segfull[i], 1);
             mbar_init(&segempty[i], kSegUsers);
@@ -434,9 +437,11 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         sg.t0 = it.t0;
                         sg.t1 = it.t1;
                         const int last_row = min(it.m * 256 + 256, it.seq.q_len * a.group);
-                        sg.has_b = last_row > it.m * 256 + kHalfRows;
-                        sg.count[0] = max(min(it.t1, tiles_until(a, it.seq, it.m * 256 + kHalfRows)) - it.t0, 0);
-                        sg.count[1] = sg.has_b ? it.t1 - it.t0 : 0;
+                        const int n = it.t1 - it.t0;
+                        sg.dual = last_row <= it.m * 256 + kHalfRows;
+                        sg.count[0] = sg.dual ? (n + 1) / 2
+                                              : max(min(it.t1, tiles_until(a, it.seq, it.m * 256 + kHalfRows)) - it.t0, 0);
+                        sg.count[1] = sg.dual ? n / 2 : n;
                         sg.row0 = it.m * 256;
                         sg.rows_end = it.seq.q_len * a.group;
                         sg.len = it.seq.len;
@@ -490,45 +495,83 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const Segment *sg = segs.next(abort_flag, status);
                 if (sg == nullptr) break;
                 const int n = sg->t1 - sg->t0, count[2] = {sg->count[0], sg->count[1]};
+                const bool dual = sg->dual;
                 mbar_arrive(&segempty[segs.i]);
                 if (++segs.i == F::kSegs) {
                     segs.i = 0;
                     segs.phase ^= 1;
                 }
-                ok = mbar_wait(&full[kstage], kphase, abort_flag, status);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (count[half] == 0) continue;
+                // scores of a half's first tile, or of its next one
+                auto first_scores = [&](int half) {
                     ok = ok && mbar_wait(&qfull[half], qphase[half], abort_flag, status);
                     qphase[half] ^= 1;
                     if (ok) scores(half);
+                };
+                auto wait_k = [&] { ok = ok && mbar_wait(&full[kstage], kphase, abort_flag, status); };
+                // O of a half from its weights and V, in two parts as the weights come
+                auto product = [&](int half, bool fresh) {
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        ok = ok && mbar_wait(&pfull[2 * half + part], pphase[half], abort_flag, status);
+                        if (!ok) return;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int s = 4 * part; s < 4 * part + 4; ++s)  // 16 positions each
+                            umma_f16_ta(tmem + F::o_col(half), tmem + F::s_col(half) + 8 * s,
+                                        umma_desc_mn_sw128(v16 + vbuf * F::kV16 + 16 * 128 * s, F::kV16 / 2),
+                                        id_o, fresh && s == 0 ? 0u : 1u);
+                    }
+                    pphase[half] ^= 1;
+                };
+                auto next_v = [&] {
+                    umma_commit(&vempty[vbuf]);
+                    vbuf ^= 1;
+                    vphase ^= vbuf ^ 1;
+                };
+                if (dual) {
+                    for (int half = 0; half < min(n, 2); ++half) {
+                        wait_k();
+                        first_scores(half);
+                        if (ok) next_k();
+                    }
+                    for (int j = 0; j < n && ok; ++j) {
+                        const int half = j & 1;
+                        ok = mbar_wait(&vfull[vbuf], vphase, abort_flag, status);
+                        if (ok) product(half, j < 2);
+                        if (!ok) break;
+                        next_v();
+                        if (j + 2 < n) {
+                            wait_k();
+                            if (!ok) break;
+                            scores(half);
+                            next_k();
+                        } else {
+                            umma_commit(&ofull[half]);
+                        }
+                    }
+                    continue;
                 }
+                wait_k();
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    if (count[half] > 0) first_scores(half);
                 if (ok) next_k();
                 for (int j = 0; j < n && ok; ++j) {
                     ok = mbar_wait(&vfull[vbuf], vphase, abort_flag, status);
-                    if (j + 1 < n) ok = ok && mbar_wait(&full[kstage], kphase, abort_flag, status);
+                    if (j + 1 < n) wait_k();
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        if (j >= count[half]) continue;
-                        ok = ok && mbar_wait(&pfull[half], pphase[half], abort_flag, status);
-                        if (!ok) break;
-                        pphase[half] ^= 1;
-                        tc_fence_after_sync();
-#pragma unroll
-                        for (int s = 0; s < 8; ++s)  // 16 positions each
-                            umma_f16_ta(tmem + F::o_col(half), tmem + F::s_col(half) + 8 * s,
-                                        umma_desc_mn_sw128(v16 + vbuf * F::kV16 + 16 * 128 * s, F::kV16 / 2),
-                                        id_o, j + s > 0 ? 1u : 0u);
+                        if (j >= count[half] || !ok) continue;
+                        product(half, j == 0);
+                        if (!ok) continue;
                         if (j + 1 < count[half])
                             scores(half);
                         else
                             umma_commit(&ofull[half]);
                     }
                     if (!ok) break;
-                    umma_commit(&vempty[vbuf]);
+                    next_v();
                     if (j + 1 < n) next_k();
-                    vbuf ^= 1;
-                    vphase ^= vbuf ^ 1;
                 }
             }
         }
@@ -594,27 +637,21 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const uint32_t s_tm = tmem + lanes + F::s_col(half), o_tm = tmem + lanes + F::o_col(half);
         const int G = a.group;
 
-        // sequences without positions, and reports
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-            if (threadIdx.x == 0 && seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
-            const Seq s = seq_of(a, b);
-            if (s.len > 0) continue;
-            const int64_t width = static_cast<int64_t>(a.q_heads) * kDim;
-            for (int64_t i = threadIdx.x; i < s.q_len * width; i += 256)
-                a.out[(s.q0 + i / width) * a.out_stride + i % width] = 0;
-            if (a.lse != nullptr)
-                for (int i = threadIdx.x; i < s.q_len * a.q_heads; i += 256)
-                    a.lse[static_cast<int64_t>(s.q0) * a.q_heads + i] = -INFINITY;
-        }
+        for (int b = blockIdx.x * 256 + threadIdx.x; b < a.B; b += gridDim.x * 256)
+            if (seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
 
         uint32_t sphase = 0, ophase = 0;
         for (;; segs.release()) {
             const Segment *sg = segs.next(abort_flag, status);
             if (sg == nullptr) break;
-            if (half == 1 && !sg->has_b) continue;
             const int n = sg->count[half];
-            const int r = sg->row0 + half * kHalfRows + ht;  // row of the sequence and head
+            const bool dual = sg->dual;
+            // this thread's row of the sequence and head; up to 64 doubled rows are
+            // in the other warps of half B, which have another scheduler
+            const int shift = dual ? (half == 1 && sg->rows_end - sg->row0 <= 64 ? 64 : 0) : half * kHalfRows;
+            const int r = sg->row0 + (dual ? (ht + shift) % kHalfRows : ht + shift);
             const bool live = r < sg->rows_end;
+            const bool any_live = __any_sync(0xFFFFFFFFu, live);
             const int tok = r / G, head = sg->hk * G + (r - tok * G);
             const int64_t q_row = sg->q0 + tok;
             float m_run = -INFINITY, l_run = 0.0f;
@@ -662,10 +699,15 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
                 // columns of tile t0 that the row sees, 128 fewer per tile
                 int seen = (live ? (a.causal ? min(sg->limit0 + tok, sg->len - 1) : sg->len - 1) : -1) + 1 -
-                           sg->t0 * kTile;
-                for (int j = 0; j < n; ++j, seen -= kTile) {
+                           (sg->t0 + (dual ? half : 0)) * kTile;
+                const int step = dual ? 2 * kTile : kTile;
+                for (int j = 0; j < n; ++j, seen -= step) {
                     mbar_wait(&sfull[half], sphase, abort_flag, status);
                     sphase ^= 1;
+                    if (!any_live) {  // what the tensor memory holds for these rows goes nowhere
+                        if (lane < 2) mbar_arrive(&pfull[2 * half + lane]);
+                        continue;
+                    }
                     tc_fence_after_sync();
                     float v[128];
 #pragma unroll
@@ -715,11 +757,11 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             p[k] = pack_f16(x.x, x.y);
                         }
                         tmem_st32(s_tm + c / 2, p);
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&pfull[2 * half + c / 64]);
                     }
-                    tmem_st_wait();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&pfull[half]);
                     sum[0] = fadd2(sum[0], sum[1]);
                     l_run += sum[0].x + sum[0].y;
                 }
@@ -728,11 +770,11 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 tc_fence_after_sync();
             }
 
-            // O times `f` (takes the 2^8 of V back), BF16
-            auto store_row = [&](float f, auto &&part) {
+            // O times `f` (which takes the 2^8 of V back) in BF16, 32 channels c0 .. c1 - 1
+            auto store_row = [&](float f, int c0, int c1, auto &&part) {
                 uint4 *out = reinterpret_cast<uint4 *>(a.out + q_row * a.out_stride + static_cast<int64_t>(head) * kDim);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
+                for (int c = c0; c < c1; ++c) {
                     float o[32];
                     part(c, o);
                     if (!live) continue;
@@ -754,59 +796,76 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 tmem_ld32(o_tm + 32 * c, o);
                 tmem_ld_wait<32>(o);
             };
-            if (sg->whole) {
-                store_row(l_run > 0.0f ? __fdividef(256.0f, l_run) : 0.0f, from_tmem);
+            if (sg->whole && !dual) {
+                store_row(l_run > 0.0f ? __fdividef(256.0f, l_run) : 0.0f, 0, 4, from_tmem);
                 store_lse(m_run, l_run);
                 continue;
             }
             // partial: this CTA's slot 1 if the item begins here, else slot 0
             const int c_first = sg->c_first, c_last = sg->c_last;
-            auto slot = [&](int i) {
-                return partials + (static_cast<int64_t>(2 * i + (i == c_first ? 1 : 0)) * 2 + half) * F::kPartial;
+            auto slot = [&](int i, int h) {
+                return partials + (static_cast<int64_t>(2 * i + (i == c_first ? 1 : 0)) * 2 + h) * F::kPartial;
             };
-            float *mine = slot(blockIdx.x);
-            if (n > 0) {
+            // contribution k is that of CTA c_first + k, or of half k % 2 of CTA c_first + k / 2;
+            // rows of doubled halves are kept by their number
+            const int ctas = c_last - c_first + 1, contributions = dual ? 2 * ctas : ctas;
+            auto contribution = [&](int k) {
+                return dual ? slot(c_first + k / 2, k & 1) : slot(c_first + k, half);
+            };
+            const int rt = dual ? r - sg->row0 : ht;
+            float *mine = slot(blockIdx.x, half);
+            if (n > 0 && any_live) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float o[32];
                     from_tmem(c, o);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        __stcg(reinterpret_cast<float4 *>(mine) + (8 * c + k) * kHalfRows + ht,
+                        __stcg(reinterpret_cast<float4 *>(mine) + (8 * c + k) * kHalfRows + rt,
                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
                 }
             }
-            __stcg(mine + kHalfRows * kDim + ht, m_run);
-            __stcg(mine + kHalfRows * (kDim + 1) + ht, l_run);
+            __stcg(mine + kHalfRows * kDim + rt, m_run);
+            __stcg(mine + kHalfRows * (kDim + 1) + rt, l_run);
             __threadfence();
-            named_barrier(1 + half, 128);
-            if (ht == 0) {
-                const int seen = atomicAdd(counters + 2 * c_first + half, 1);
-                shared_last[half] = seen == c_last - c_first;
-                if (shared_last[half]) counters[2 * c_first + half] = 0;
-                __threadfence();
+            // doubled halves arrive (and join) as one
+            const uint32_t bar = dual ? 3 : 1 + half, threads = dual ? 256 : 128;
+            const int word = dual ? 2 : half;
+            named_barrier(bar, threads);
+            if (dual ? threadIdx.x == 0 : ht == 0) {
+                int *counter = counters + 3 * c_first + word;
+                bool last = true;
+                if (ctas > 1) {
+                    last = atomicAdd(counter, 1) == ctas - 1;
+                    if (last) *counter = 0;
+                    __threadfence();
+                }
+                shared_last[word] = last;
             }
-            named_barrier(1 + half, 128);
-            if (!shared_last[half]) continue;
+            named_barrier(bar, threads);
+            if (!shared_last[word]) continue;
             // join in the order of the CTAs, a row per thread
             float m = -INFINITY, l = 0.0f;
-            for (int i = c_first; i <= c_last; ++i) m = fmaxf(m, __ldcg(slot(i) + kHalfRows * kDim + ht));
-            for (int i = c_first; i <= c_last && m > -INFINITY; ++i) {
-                const float *p = slot(i) + kHalfRows * kDim + ht;
+            for (int k = 0; k < contributions; ++k)
+                m = fmaxf(m, __ldcg(contribution(k) + kHalfRows * kDim + rt));
+            for (int k = 0; k < contributions && m > -INFINITY; ++k) {
+                const float *p = contribution(k) + kHalfRows * kDim + rt;
                 l = fmaf(ex2(__ldcg(p) - m), __ldcg(p + kHalfRows), l);
             }
-            store_row(l > 0.0f ? __fdividef(256.0f, l) : 0.0f, [&](int c, float *o) {
+            // doubled halves: each half the channels of its number
+            store_row(l > 0.0f ? __fdividef(256.0f, l) : 0.0f, dual ? 2 * half : 0, dual ? 2 * half + 2 : 4,
+                      [&](int c, float *o) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = 0.0f;
                 if (l <= 0.0f) return;
-                for (int i = c_first; i <= c_last; ++i) {
-                    const float *p = slot(i);
-                    const float mi = __ldcg(p + kHalfRows * kDim + ht);
+                for (int i = 0; i < contributions; ++i) {
+                    const float *p = contribution(i);
+                    const float mi = __ldcg(p + kHalfRows * kDim + rt);
                     if (mi == -INFINITY) continue;  // its O may never have been written
                     const float f = ex2(mi - m);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p) + (8 * c + k) * kHalfRows + ht);
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p) + (8 * c + k) * kHalfRows + rt);
                         o[4 * k] = fmaf(f, v.x, o[4 * k]);
                         o[4 * k + 1] = fmaf(f, v.y, o[4 * k + 1]);
                         o[4 * k + 2] = fmaf(f, v.z, o[4 * k + 2]);
@@ -814,7 +873,8 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
                 }
             });
-            store_lse(m, l);
+            if (!dual || half == 0) store_lse(m, l);
+            if (dual) named_barrier(bar, threads);  // the next partial may take the same slot
         }
     }
     tc_fence_before_sync();

@@ -679,33 +679,30 @@ size_t silu_ws_bytes(int64_t M, int64_t I) {
 
 // ---------------------------------------------------------------- norm, rotary, attention
 
-constexpr int64_t kNormMaxK = int64_t(kNormMaxThreads) * 4 * 8;  // 4 vectors of 8 per thread
+constexpr int64_t kNormMaxK = 32768;  // 1024 threads of 4 vectors of 8
 constexpr int64_t kRopeMaxHeads = 1024;
 
-template <int V>
-cudaError_t launch_rms_norm_v(const DeviceInfo &d, const void *x, const void *residual,
+template <int V, int kMaxThreads, int kMinCtas>
+cudaError_t launch_rms_norm_v(const void *x, const void *residual,
                               const void *weight, float eps, int64_t M, int64_t K,
                               void *residual_out, uint8_t *q, float *s, void *h, cudaStream_t st) {
     const int nvec = static_cast<int>(K / 8);
     const int threads = ((nvec + V - 1) / V + 31) / 32 * 32;
-    const int64_t per_sm = std::max(1, 2048 / threads);
-    const int64_t grid = std::min<int64_t>(M, d.sm_count * per_sm);
-    return launch(rms_norm_kernel<V>, dim3(static_cast<unsigned>(grid)),
+    return launch(rms_norm_kernel<V, kMaxThreads, kMinCtas>, dim3(static_cast<unsigned>(M)),
                   dim3(static_cast<unsigned>(threads)), 0, st, static_cast<const uint4 *>(x),
-                  static_cast<const uint4 *>(residual), static_cast<const uint4 *>(weight), eps, M,
-                  nvec, static_cast<uint4 *>(residual_out), reinterpret_cast<uint2 *>(q), s,
+                  static_cast<const uint4 *>(residual), static_cast<const uint4 *>(weight), eps, nvec,
+                  static_cast<uint4 *>(residual_out), reinterpret_cast<uint2 *>(q), s,
                   static_cast<uint4 *>(h));
 }
 
 cudaError_t launch_rms_norm(const DeviceInfo &d, const void *x, const void *residual,
                             const void *weight, float eps, int64_t M, int64_t K, void *residual_out,
                             uint8_t *q, float *s, void *h, cudaStream_t st) {
-    const int64_t nvec = K / 8;
-    if (nvec <= kNormMaxThreads)
-        return launch_rms_norm_v<1>(d, x, residual, weight, eps, M, K, residual_out, q, s, h, st);
-    if (nvec <= 2 * kNormMaxThreads)
-        return launch_rms_norm_v<2>(d, x, residual, weight, eps, M, K, residual_out, q, s, h, st);
-    return launch_rms_norm_v<4>(d, x, residual, weight, eps, M, K, residual_out, q, s, h, st);
+    if (M <= d.sm_count && K <= 8192)
+        return launch_rms_norm_v<1, 1024, 1>(x, residual, weight, eps, M, K, residual_out, q, s, h, st);
+    if (K <= 8192)
+        return launch_rms_norm_v<2, 512, 3>(x, residual, weight, eps, M, K, residual_out, q, s, h, st);
+    return launch_rms_norm_v<4, 1024, 1>(x, residual, weight, eps, M, K, residual_out, q, s, h, st);
 }
 
 // Cache positions of one sequence: 32-bit in the kernels, with room for a tile.
@@ -1013,8 +1010,10 @@ fp8bq_status fp8bq_rope_kv_write_e4m3(const void *qkv_bf16, int64_t row_stride, 
     a.dim = static_cast<int>(head_dim);
     a.rot = static_cast<int>(rot_dim);
     a.interleaved = interleaved != 0;
-    a.tok = T >= static_cast<int64_t>(d->sm_count) * 16 ? kRopeMaxTok : 1;
-    return from_cuda(launch(rope_kv_write_kernel, dim3(static_cast<unsigned>((T + a.tok - 1) / a.tok)),
+    // few tokens: a whole CTA each, for the shortest chain
+    a.span = T >= static_cast<int64_t>(d->sm_count) * 8 ? kRopeMinSpan : kRopeThreads;
+    const int64_t toks = kRopeThreads / a.span;
+    return from_cuda(launch(rope_kv_write_kernel, dim3(static_cast<unsigned>((T + toks - 1) / toks)),
                             dim3(kRopeThreads), 0, static_cast<cudaStream_t>(stream), a, d->status));
 }
 

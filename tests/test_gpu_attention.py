@@ -84,7 +84,11 @@ def test_few_tokens(q_lens, ctx, heads, page, causal):
 @pytest.mark.parametrize("q_lens,ctx,heads,page", [
     ([128], [128], (7, 1), 64), ([129], [300], (8, 8), 16), ([37], [37], (14, 2), 8),
     ([100, 1, 250], [100, 513, 700], (28, 4), 128), ([19, 0, 65, 40], [3, 0, 65, 0], (56, 8), 32),
-    ([257], [1000], (6, 2), 256), ([200], [5000], (8, 1), 64)])
+    ([257], [1000], (6, 2), 256), ([200], [5000], (8, 1), 64),
+    # blocks of up to 64, 128 and 256 rows, whole and split, several for each CTA
+    ([5 + i % 15 for i in range(40)], [29 * i % 1200 for i in range(40)], (56, 8), 16),
+    ([40 + i % 60 for i in range(24)], [37 * i % 1000 for i in range(24)], (28, 4), 64),
+    ([5] * 3, [9000, 3, 4000], (56, 8), 64), ([600] * 2, [600, 0], (8, 8), 128)])
 def test_chunks(q_lens, ctx, heads, page, causal):
     c = ref.random_batch(q_lens, ctx, *heads, page, 70 + len(ctx))
     check(c, *run(c, *heads, page, causal, pad_rows=1), *heads, page, causal)
