@@ -21,7 +21,8 @@
 // F16 and FP32), so O is hardly ever rescaled in the tensor memory.
 //
 // Blocks of at most 128 rows have no second half: there both halves hold the same
-// rows and take the tiles in turn, and are joined like two CTAs.
+// rows and take the tiles in turn; B hands its result to A through the shared
+// memory of the queries.
 //
 // Work is a list of K/V tiles ordered by (sequence, 256 rows, kv head, tile),
 // each (rows, head) item preceded by kItemCost tiles' worth of nothing; CTA c of
@@ -63,7 +64,8 @@ struct Many {
     static constexpr int kBars = 2 * kStages + 14 + 2 * kSegs;
     static constexpr int kSegOff = kBarOff + kBars * 8;
     static constexpr int kMiscOff = kSegOff + kSegs * 64;
-    static constexpr int kBytes = kMiscOff + 256 + 1024;
+    static constexpr int kRowOff = kMiscOff + 256;  // maximum and sum of half B's rows
+    static constexpr int kBytes = kRowOff + 2 * kHalfRows * 4 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory");
     // floats of one half's partial: O [32 groups of 4 channels][128 rows][4], max, sum [128]
     static constexpr int kPartial = kHalfRows * (kDim + 2);
@@ -284,7 +286,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + F::kMiscOff);
     uint32_t *tmem_slot = misc;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
-    int *shared_last = reinterpret_cast<int *>(misc + 2);      // of half A, half B, doubled halves
+    int *shared_last = reinterpret_cast<int *>(misc + 2);      // [2]
     int *start_bm = reinterpret_cast<int *>(misc + 5);         // sequence, block
     int *parts = reinterpret_cast<int *>(misc + 7);            // CTAs that have a part
     int64_t *start_w = reinterpret_cast<int64_t *>(misc + 8);  // w0, w1, base, total
@@ -671,13 +673,18 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const float scale =
                     a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
                 uint8_t *dst = smem + 2 * half * F::kQPart + ht * kDim;
-#pragma unroll
+                // not unrolled (the vectors move down the array instead): the first
+                // pass over the unrolled code fetched it for 5 us
+#pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
+                    const uint4 pair[2] = {u[0], u[1]};
+#pragma unroll
+                    for (int k = 0; k < 14; ++k) u[k] = u[k + 2];
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int d = 0; d < 2; ++d) {
                         float f[8];
-                        unpack_bf16x8(u[2 * c + d], f);
+                        unpack_bf16x8(pair[d], f);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const float x0 = f[4 * k] * up, x1 = f[4 * k + 1] * up;
@@ -770,21 +777,66 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 tc_fence_after_sync();
             }
 
-            // O times `f` (which takes the 2^8 of V back) in BF16, 32 channels c0 .. c1 - 1
-            auto store_row = [&](float f, int c0, int c1, auto &&part) {
-                uint4 *out = reinterpret_cast<uint4 *>(a.out + q_row * a.out_stride + static_cast<int64_t>(head) * kDim);
+            float *b_max = reinterpret_cast<float *>(smem + F::kRowOff), *b_sum = b_max + kHalfRows;
+            float4 *b_out = reinterpret_cast<float4 *>(smem);  // [32 groups of 4 channels][128 rows]
+            float f_a = 1.0f, f_b = 0.0f;
+            if (dual) {
+                named_barrier(3, 256);  // both halves' MMAs are done with the queries
+                if (half == 1) {
+                    const int row = r - sg->row0;
+                    if (n > 0 && any_live) {
 #pragma unroll 1
-                for (int c = c0; c < c1; ++c) {
-                    float o[32];
-                    part(c, o);
-                    if (!live) continue;
+                        for (int c = 0; c < 4; ++c) {
+                            float o[32];
+                            tmem_ld32(o_tm + 32 * c, o);
+                            tmem_ld_wait<32>(o);
+                            if (live) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float t[8];
-#pragma unroll
-                        for (int d = 0; d < 8; ++d) t[d] = f != 0.0f ? o[8 * k + d] * f : 0.0f;
-                        out[4 * c + k] = pack_bf16x8(t);
+                                for (int k = 0; k < 8; ++k)
+                                    b_out[(8 * c + k) * kHalfRows + row] =
+                                        make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            }
+                        }
                     }
+                    b_max[row] = m_run;
+                    b_sum[row] = l_run;
+                    named_barrier(3, 256);
+                    named_barrier(3, 256);  // half A has read it
+                    continue;
+                }
+                named_barrier(3, 256);
+                const float m_b = b_max[ht], m = fmaxf(m_run, m_b);
+                if (m_b > -INFINITY) {
+                    f_a = ex2(m_run - m);
+                    f_b = ex2(m_b - m);
+                    l_run = fmaf(l_run, f_a, b_sum[ht] * f_b);
+                    m_run = m;
+                }
+            }
+            // O of this thread's row, 32 channels from 32 c on, with half B's where there is one
+            auto output = [&](int c, float *o) {
+                tmem_ld32(o_tm + 32 * c, o);
+                tmem_ld_wait<32>(o);
+                if (f_b == 0.0f) return;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float4 v = b_out[(8 * c + k) * kHalfRows + ht];
+                    o[4 * k] = fmaf(o[4 * k], f_a, v.x * f_b);
+                    o[4 * k + 1] = fmaf(o[4 * k + 1], f_a, v.y * f_b);
+                    o[4 * k + 2] = fmaf(o[4 * k + 2], f_a, v.z * f_b);
+                    o[4 * k + 3] = fmaf(o[4 * k + 3], f_a, v.w * f_b);
+                }
+            };
+            // 32 channels of the output: o times `f` (which takes the 2^8 of V back) in BF16
+            auto store = [&](int c, const float *o, float f) {
+                if (!live) return;
+                uint4 *out = reinterpret_cast<uint4 *>(a.out + q_row * a.out_stride + static_cast<int64_t>(head) * kDim) + 4 * c;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float t[8];
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) t[d] = f != 0.0f ? o[8 * k + d] * f : 0.0f;
+                    out[k] = pack_bf16x8(t);
                 }
             };
             auto store_lse = [&](float m, float l) {
@@ -792,89 +844,87 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     a.lse[q_row * a.q_heads + head] =
                         l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
             };
-            auto from_tmem = [&](int c, float *o) {
-                tmem_ld32(o_tm + 32 * c, o);
-                tmem_ld_wait<32>(o);
-            };
-            if (sg->whole && !dual) {
-                store_row(l_run > 0.0f ? __fdividef(256.0f, l_run) : 0.0f, 0, 4, from_tmem);
+            if (sg->whole) {
+                const float f = l_run > 0.0f ? __fdividef(256.0f, l_run) : 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    output(c, o);
+                    store(c, o, f);
+                }
                 store_lse(m_run, l_run);
+                if (dual) named_barrier(3, 256);
                 continue;
             }
             // partial: this CTA's slot 1 if the item begins here, else slot 0
             const int c_first = sg->c_first, c_last = sg->c_last;
-            auto slot = [&](int i, int h) {
-                return partials + (static_cast<int64_t>(2 * i + (i == c_first ? 1 : 0)) * 2 + h) * F::kPartial;
+            auto slot = [&](int i) {
+                return partials + (static_cast<int64_t>(2 * i + (i == c_first ? 1 : 0)) * 2 + half) * F::kPartial;
             };
-            // contribution k is that of CTA c_first + k, or of half k % 2 of CTA c_first + k / 2;
-            // rows of doubled halves are kept by their number
-            const int ctas = c_last - c_first + 1, contributions = dual ? 2 * ctas : ctas;
-            auto contribution = [&](int k) {
-                return dual ? slot(c_first + k / 2, k & 1) : slot(c_first + k, half);
-            };
-            const int rt = dual ? r - sg->row0 : ht;
-            float *mine = slot(blockIdx.x, half);
+            float *mine = slot(blockIdx.x);
             if (n > 0 && any_live) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float o[32];
-                    from_tmem(c, o);
+                    output(c, o);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        __stcg(reinterpret_cast<float4 *>(mine) + (8 * c + k) * kHalfRows + rt,
+                        __stcg(reinterpret_cast<float4 *>(mine) + (8 * c + k) * kHalfRows + ht,
                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
                 }
             }
-            __stcg(mine + kHalfRows * kDim + rt, m_run);
-            __stcg(mine + kHalfRows * (kDim + 1) + rt, l_run);
+            __stcg(mine + kHalfRows * kDim + ht, m_run);
+            __stcg(mine + kHalfRows * (kDim + 1) + ht, l_run);
+            if (dual) named_barrier(3, 256);
             __threadfence();
-            // doubled halves arrive (and join) as one
-            const uint32_t bar = dual ? 3 : 1 + half, threads = dual ? 256 : 128;
-            const int word = dual ? 2 : half;
-            named_barrier(bar, threads);
-            if (dual ? threadIdx.x == 0 : ht == 0) {
-                int *counter = counters + 3 * c_first + word;
-                bool last = true;
-                if (ctas > 1) {
-                    last = atomicAdd(counter, 1) == ctas - 1;
-                    if (last) *counter = 0;
-                    __threadfence();
-                }
-                shared_last[word] = last;
+            named_barrier(1 + half, 128);
+            if (ht == 0) {
+                int *counter = counters + 2 * c_first + half;
+                const bool last = atomicAdd(counter, 1) == c_last - c_first;
+                if (last) *counter = 0;
+                shared_last[half] = last;
+                __threadfence();
             }
-            named_barrier(bar, threads);
-            if (!shared_last[word]) continue;
+            named_barrier(1 + half, 128);
+            if (!shared_last[half] || !any_live) continue;
             // join in the order of the CTAs, a row per thread
             float m = -INFINITY, l = 0.0f;
-            for (int k = 0; k < contributions; ++k)
-                m = fmaxf(m, __ldcg(contribution(k) + kHalfRows * kDim + rt));
-            for (int k = 0; k < contributions && m > -INFINITY; ++k) {
-                const float *p = contribution(k) + kHalfRows * kDim + rt;
-                l = fmaf(ex2(__ldcg(p) - m), __ldcg(p + kHalfRows), l);
+#pragma unroll 4
+            for (int i = c_first; i <= c_last; ++i) m = fmaxf(m, __ldcg(slot(i) + kHalfRows * kDim + ht));
+#pragma unroll 4
+            for (int i = c_first; i <= c_last; ++i) {
+                const float *p = slot(i) + kHalfRows * kDim + ht;
+                const float mi = __ldcg(p), li = __ldcg(p + kHalfRows);
+                l += mi > -INFINITY ? ex2(mi - m) * li : 0.0f;
             }
-            // doubled halves: each half the channels of its number
-            store_row(l > 0.0f ? __fdividef(256.0f, l) : 0.0f, dual ? 2 * half : 0, dual ? 2 * half + 2 : 4,
-                      [&](int c, float *o) {
+            const float f = l > 0.0f ? __fdividef(256.0f, l) : 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float o[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = 0.0f;
-                if (l <= 0.0f) return;
-                for (int i = 0; i < contributions; ++i) {
-                    const float *p = contribution(i);
-                    const float mi = __ldcg(p + kHalfRows * kDim + rt);
-                    if (mi == -INFINITY) continue;  // its O may never have been written
-                    const float f = ex2(mi - m);
+#pragma unroll 2
+                for (int i = c_first; i <= c_last; ++i) {
+                    const float *p = slot(i);
+                    const float mi = __ldcg(p + kHalfRows * kDim + ht);
+                    float4 v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = __ldcg(reinterpret_cast<const float4 *>(p) + (8 * c + k) * kHalfRows + ht);
+                    // without a maximum, its O may never have been written
+                    const bool some = mi > -INFINITY;
+                    const float fi = ex2(mi - m);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p) + (8 * c + k) * kHalfRows + rt);
-                        o[4 * k] = fmaf(f, v.x, o[4 * k]);
-                        o[4 * k + 1] = fmaf(f, v.y, o[4 * k + 1]);
-                        o[4 * k + 2] = fmaf(f, v.z, o[4 * k + 2]);
-                        o[4 * k + 3] = fmaf(f, v.w, o[4 * k + 3]);
+                        o[4 * k] = some ? fmaf(fi, v[k].x, o[4 * k]) : o[4 * k];
+                        o[4 * k + 1] = some ? fmaf(fi, v[k].y, o[4 * k + 1]) : o[4 * k + 1];
+                        o[4 * k + 2] = some ? fmaf(fi, v[k].z, o[4 * k + 2]) : o[4 * k + 2];
+                        o[4 * k + 3] = some ? fmaf(fi, v[k].w, o[4 * k + 3]) : o[4 * k + 3];
                     }
                 }
-            });
-            if (!dual || half == 0) store_lse(m, l);
-            if (dual) named_barrier(bar, threads);  // the next partial may take the same slot
+                store(c, o, f);
+            }
+            store_lse(m, l);
         }
     }
     tc_fence_before_sync();
