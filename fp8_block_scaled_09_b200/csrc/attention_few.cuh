@@ -414,79 +414,88 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_wait(&full[i % F::kStages], (i / F::kStages) & 1, nullptr, status);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            Chunks<NR> ahead = cur;
-            bool more = ahead.next();
-            const uint32_t id_s = umma_idesc_e4m3(kTile, N), id_o = idesc_e4m3_mn(kDim, N);
-            uint32_t stage = 0, phase = 0;
-            uint32_t pslot[2] = {0, 0}, pphase[2] = {0, 0};  // of each softmax group
-            uint32_t gk = 0, gv = 0, segs = 0;  // chunks and segments so far
-            bool ok = true;
-            auto advance = [&] {
-                if (++stage == F::kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            };
-            auto scores = [&](const Chunks<NR> &c) {
-                if (c.first) {
-                    ok = ok && mbar_wait(&qfull[segs & 3], (segs >> 2) & 1, abort_flag, status);
-                    ++segs;
-                }
-                const uint32_t buf = gk & 1;
-                ok = ok && mbar_wait(&sfree[buf], ((gk >> 1) & 1) ^ 1, abort_flag, status);
-                const uint32_t q = smem_addr(smem + F::kQOff + ((segs - 1) & 1) * F::kQ);
-                for (int j = 0; j < c.n && ok; ++j) {
-                    ok = mbar_wait(&full[stage], phase, abort_flag, status);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t k = smem_addr(smem + stage * kStageBytes);
+        Chunks<NR> ahead = cur;
+        bool more = ahead.next();
+        const uint32_t id_s = umma_idesc_e4m3(kTile, N), id_o = idesc_e4m3_mn(kDim, N);
+        // descriptors: an address step of 16 bytes is 1
+        const uint64_t ring_desc = umma_desc_sw128(smem_addr(smem)),
+                       q_desc = umma_desc_sw128(smem_addr(smem + F::kQOff)),
+                       p_desc = umma_desc_mn(smem_addr(smem + F::kPOff), kTile * 16, 128);
+        uint32_t stage = 0, phase = 0;
+        uint32_t pslot[2] = {0, 0}, pphase[2] = {0, 0};  // of each softmax group
+        uint32_t gk = 0, gv = 0, segs = 0;  // chunks and segments so far
+        bool ok = true;
+        auto advance = [&] {
+            if (++stage == F::kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        };
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = ok && mbar_wait(bar, parity, abort_flag, status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+        };
+        auto scores = [&](const Chunks<NR> &c) {
+            if (c.first) {
+                wait(&qfull[segs & 3], (segs >> 2) & 1);
+                ++segs;
+            }
+            const uint32_t buf = gk & 1;
+            wait(&sfree[buf], ((gk >> 1) & 1) ^ 1);
+            const uint64_t q = q_desc + ((segs - 1) & 1) * (F::kQ / 16);
+            for (int j = 0; j < c.n && ok; ++j) {
+                wait(&full[stage], phase);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint64_t k = ring_desc + stage * (kStageBytes / 16);
+                const uint32_t d = tmem + F::s_col(buf, j);
+                if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        umma_e4m3(tmem + F::s_col(buf, j), umma_desc_sw128(k + 32 * s),
-                                  umma_desc_sw128(q + 32 * s), id_s, s > 0 ? 1u : 0u);
+                    for (int s = 0; s < 4; ++s) umma_e4m3(d, k + 2 * s, q + 2 * s, id_s, s > 0 ? 1u : 0u);
                     umma_commit(&empty[stage]);
-                    advance();
-                }
-                if (ok) {
-                    umma_commit(&sfull[buf]);
-                    if (c.last) umma_commit(&qempty[(segs - 1) & 1]);
-                }
-                ++gk;
-            };
-            if (more) scores(ahead);
-            while (ok && cur.next()) {
-                more = ahead.next();
-                if (more) scores(ahead);
-                const uint32_t buf = gv & 1;
-                ok = ok && mbar_wait(&ofree[buf], ((gv >> 1) & 1) ^ 1, abort_flag, status);
-                for (int j = 0; j < cur.n && ok; ++j) {
-                    const int h = j & 1;
-                    const uint32_t slot = h * F::kGroupSlots + pslot[h];
-                    ok = mbar_wait(&full[stage], phase, abort_flag, status);
-                    // the sequence ends in this tile: its softmax group clears what is behind
-                    if (ok && (cur.t + j + 1) * kTile > cur.seq.len) mbar_arrive(&vready[h]);
-                    ok = ok && mbar_wait(&pfull[slot], pphase[h], abort_flag, status);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t v = smem_addr(smem + stage * kStageBytes);
-                    const uint32_t p = smem_addr(smem + F::kPOff + slot * F::kP);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)  // 32 positions each
-                        umma_e4m3(tmem + F::o_col(buf), umma_desc_sw128(v + 32 * kDim * s),
-                                  umma_desc_mn(p + 32 * 16 * s, kTile * 16, 128), id_o,
-                                  j + s > 0 ? 1u : 0u);
-                    umma_commit(&empty[stage]);
-                    umma_commit(&pempty[slot]);
-                    advance();
-                    if (++pslot[h] == F::kGroupSlots) {
-                        pslot[h] = 0;
-                        pphase[h] ^= 1;
+                    if (j == c.n - 1) {
+                        umma_commit(&sfull[buf]);
+                        if (c.last) umma_commit(&qempty[(segs - 1) & 1]);
                     }
                 }
-                if (ok) umma_commit(&ofull[buf]);
-                ++gv;
+                __syncwarp();
+                advance();
             }
+            ++gk;
+        };
+        if (more) scores(ahead);
+        while (ok && cur.next()) {
+            more = ahead.next();
+            if (more) scores(ahead);
+            const uint32_t buf = gv & 1;
+            wait(&ofree[buf], ((gv >> 1) & 1) ^ 1);
+            for (int j = 0; j < cur.n && ok; ++j) {
+                const int h = j & 1;
+                const uint32_t slot = h * F::kGroupSlots + pslot[h];
+                wait(&full[stage], phase);
+                // the sequence ends in this tile: its softmax group clears what is behind
+                if (ok && (cur.t + j + 1) * kTile > cur.seq.len && lane == 0) mbar_arrive(&vready[h]);
+                wait(&pfull[slot], pphase[h]);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint64_t v = ring_desc + stage * (kStageBytes / 16), p = p_desc + slot * (F::kP / 16);
+                const uint32_t d = tmem + F::o_col(buf), first = j > 0 ? 1u : 0u;
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)  // 32 positions each
+                        umma_e4m3(d, v + 2 * kDim * s, p + 32 * s, id_o, s > 0 ? 1u : first);
+                    umma_commit(&empty[stage]);
+                    umma_commit(&pempty[slot]);
+                    if (j == cur.n - 1) umma_commit(&ofull[buf]);
+                }
+                __syncwarp();
+                advance();
+                if (++pslot[h] == F::kGroupSlots) {
+                    pslot[h] = 0;
+                    pphase[h] ^= 1;
+                }
+            }
+            ++gv;
         }
     } else if (warp == 2 + kFewSoftmaxWarps) {
         // ------------------------------------------------------------ queries

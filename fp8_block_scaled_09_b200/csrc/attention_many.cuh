@@ -471,62 +471,75 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             uint32_t kstage = 0, kphase = 0, vbuf = 0, vphase = 0;
             uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0};
             bool ok = true;
-            const uint32_t q_addr = smem_addr(smem), ring = smem_addr(smem + F::kRingOff),
-                           v16 = smem_addr(smem + F::kV16Off);
+            // descriptors: an address step of 16 bytes is 1
+            const uint64_t q_desc = umma_desc_sw128(smem_addr(smem)),
+                           ring_desc = umma_desc_sw128(smem_addr(smem + F::kRingOff)),
+                           v_desc = umma_desc_mn_sw128(smem_addr(smem + F::kV16Off), F::kV16 / 2);
             auto scores = [&](int half) {
                 tc_fence_after_sync();
-                const uint32_t k = ring + kstage * kStageBytes;
+                const uint64_t q = q_desc + half * (2 * F::kQPart / 16),
+                               k = ring_desc + kstage * (kStageBytes / 16);
+                if (elect_one()) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        umma_e4m3(tmem + F::s_col(half),
-                                  umma_desc_sw128(q_addr + (2 * half + part) * F::kQPart + 32 * s),
-                                  umma_desc_sw128(k + 32 * s), id_s, part + s > 0 ? 1u : 0u);
-                umma_commit(&sfull[half]);
+                        for (int s = 0; s < 4; ++s)
+                            umma_e4m3(tmem + F::s_col(half), q + part * (F::kQPart / 16) + 2 * s,
+                                      k + 2 * s, id_s, part + s > 0 ? 1u : 0u);
+                    umma_commit(&sfull[half]);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (elect_one()) umma_commit(bar);
+                __syncwarp();
             };
             auto next_k = [&] {
-                umma_commit(&empty[kstage]);
+                commit(&empty[kstage]);
                 kstage += 2;
                 if (kstage == F::kStages) {
                     kstage = 0;
                     kphase ^= 1;
                 }
             };
-            while (ok && lane == 0) {
+            while (ok) {
                 const Segment *sg = segs.next(abort_flag, status);
-                if (sg == nullptr) break;
+                if (!__all_sync(0xFFFFFFFFu, sg != nullptr)) break;
                 const int n = sg->t1 - sg->t0, count[2] = {sg->count[0], sg->count[1]};
                 const bool dual = sg->dual;
-                mbar_arrive(&segempty[segs.i]);
-                if (++segs.i == F::kSegs) {
-                    segs.i = 0;
-                    segs.phase ^= 1;
-                }
+                segs.release();
+                auto wait = [&](uint64_t *bar, uint32_t phase) {
+                    ok = ok && mbar_wait(bar, phase, abort_flag, status);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                };
                 // scores of a half's first tile, or of its next one
                 auto first_scores = [&](int half) {
-                    ok = ok && mbar_wait(&qfull[half], qphase[half], abort_flag, status);
+                    wait(&qfull[half], qphase[half]);
                     qphase[half] ^= 1;
                     if (ok) scores(half);
                 };
-                auto wait_k = [&] { ok = ok && mbar_wait(&full[kstage], kphase, abort_flag, status); };
+                auto wait_k = [&] { wait(&full[kstage], kphase); };
                 // O of a half from its weights and V, in two parts as the weights come
                 auto product = [&](int half, bool fresh) {
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
-                        ok = ok && mbar_wait(&pfull[2 * half + part], pphase[half], abort_flag, status);
+                        wait(&pfull[2 * half + part], pphase[half]);
                         if (!ok) return;
                         tc_fence_after_sync();
+                        const uint64_t v = v_desc + vbuf * (F::kV16 / 16);
+                        const uint32_t first = fresh ? 0u : 1u;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int s = 4 * part; s < 4 * part + 4; ++s)  // 16 positions each
-                            umma_f16_ta(tmem + F::o_col(half), tmem + F::s_col(half) + 8 * s,
-                                        umma_desc_mn_sw128(v16 + vbuf * F::kV16 + 16 * 128 * s, F::kV16 / 2),
-                                        id_o, fresh && s == 0 ? 0u : 1u);
+                            for (int s = 4 * part; s < 4 * part + 4; ++s)  // 16 positions each
+                                umma_f16_ta(tmem + F::o_col(half), tmem + F::s_col(half) + 8 * s,
+                                            v + 128 * s, id_o, s == 0 ? first : 1u);
+                        }
+                        __syncwarp();
                     }
                     pphase[half] ^= 1;
                 };
                 auto next_v = [&] {
-                    umma_commit(&vempty[vbuf]);
+                    commit(&vempty[vbuf]);
                     vbuf ^= 1;
                     vphase ^= vbuf ^ 1;
                 };
@@ -538,7 +551,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
                     for (int j = 0; j < n && ok; ++j) {
                         const int half = j & 1;
-                        ok = mbar_wait(&vfull[vbuf], vphase, abort_flag, status);
+                        wait(&vfull[vbuf], vphase);
                         if (ok) product(half, j < 2);
                         if (!ok) break;
                         next_v();
@@ -548,7 +561,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             scores(half);
                             next_k();
                         } else {
-                            umma_commit(&ofull[half]);
+                            commit(&ofull[half]);
                         }
                     }
                     continue;
@@ -559,7 +572,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     if (count[half] > 0) first_scores(half);
                 if (ok) next_k();
                 for (int j = 0; j < n && ok; ++j) {
-                    ok = mbar_wait(&vfull[vbuf], vphase, abort_flag, status);
+                    wait(&vfull[vbuf], vphase);
                     if (j + 1 < n) wait_k();
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -569,7 +582,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         if (j + 1 < count[half])
                             scores(half);
                         else
-                            umma_commit(&ofull[half]);
+                            commit(&ofull[half]);
                     }
                     if (!ok) break;
                     next_v();
