@@ -490,12 +490,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 __syncwarp();
             };
-            auto commit = [&](uint64_t *bar) {
-                if (elect_one()) umma_commit(bar);
-                __syncwarp();
-            };
             auto next_k = [&] {
-                commit(&empty[kstage]);
                 kstage += 2;
                 if (kstage == F::kStages) {
                     kstage = 0;
@@ -518,6 +513,10 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     qphase[half] ^= 1;
                     if (ok) scores(half);
                 };
+                auto finish = [&](int half) {
+                    if (elect_one()) umma_commit(&ofull[half]);
+                    __syncwarp();
+                };
                 auto wait_k = [&] { wait(&full[kstage], kphase); };
                 // O of a half from its weights and V, in two parts as the weights come
                 auto product = [&](int half, bool fresh) {
@@ -539,7 +538,6 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     pphase[half] ^= 1;
                 };
                 auto next_v = [&] {
-                    commit(&vempty[vbuf]);
                     vbuf ^= 1;
                     vphase ^= vbuf ^ 1;
                 };
@@ -561,7 +559,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             scores(half);
                             next_k();
                         } else {
-                            commit(&ofull[half]);
+                            finish(half);
                         }
                     }
                     continue;
@@ -572,8 +570,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     if (count[half] > 0) first_scores(half);
                 if (ok) next_k();
                 for (int j = 0; j < n && ok; ++j) {
-                    wait(&vfull[vbuf], vphase);
-                    if (j + 1 < n) wait_k();
+                    wait(&vfull[vbuf], vphase);  // which also stands for the next K
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         if (j >= count[half] || !ok) continue;
@@ -582,7 +579,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         if (j + 1 < count[half])
                             scores(half);
                         else
-                            commit(&ofull[half]);
+                            finish(half);
                     }
                     if (!ok) break;
                     next_v();
@@ -594,14 +591,23 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
         // ------------------------------------------------------------ V to F16
         const int row = threadIdx.x - 256;  // position in the tile
-        uint32_t stage = 1, phase = 0, vbuf = 0, vphase = 0;
+        uint32_t stage = 1, phase = 0, vbuf = 0, vphase = 0, kstage = 0, kphase = 0;
         bool ok = true;
+        auto next_k = [&] {
+            kstage += 2;
+            if (kstage == F::kStages) {
+                kstage = 0;
+                kphase ^= 1;
+            }
+        };
         while (ok) {
             const Segment *sg = segs.next(abort_flag, status);
             if (!__all_sync(0xFFFFFFFFu, sg != nullptr)) break;
             const int t1 = sg->t1, len = sg->len;
+            const bool dual = sg->dual;
             int t = sg->t0;
             segs.release();
+            next_k();
             for (; t < t1 && ok; ++t) {
                 ok = mbar_wait(&full[stage], phase, abort_flag, status) &&
                      mbar_wait(&vempty[vbuf], vphase ^ 1, abort_flag, status);
@@ -628,6 +634,13 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     *reinterpret_cast<uint4 *>(d + (((cc + 1) ^ x) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
                 }
                 fence_proxy_async_smem();
+                if (t + 1 < t1) {
+                    // the issuer needs the next K too: one wait less for it.  (The
+                    // K before that in the same stage has been used: the V buffer
+                    // taken above was released after it.)
+                    if (!dual) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[kstage], kphase, abort_flag, status));
+                    next_k();
+                }
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&vfull[vbuf]);
@@ -656,6 +669,11 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
 
         uint32_t sphase = 0, ophase = 0;
+        uint32_t kstage = 0, vbuf = 0;  // of the segment's first tile
+        // K and V are released here, by one warp of the half that used a tile last
+        // (a commit costs the issuer ~175 cycles): a half's scores are complete after
+        // the product and the scores issued before them.
+        const bool releases = (warp & 3) == 0 && lane == 0;
         for (;; segs.release()) {
             const Segment *sg = segs.next(abort_flag, status);
             if (sg == nullptr) break;
@@ -724,6 +742,11 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 for (int j = 0; j < n; ++j, seen -= step) {
                     mbar_wait(&sfull[half], sphase, abort_flag, status);
                     sphase ^= 1;
+                    if (releases && (dual || half == 1)) {
+                        const int t = dual ? 2 * j + half : j;
+                        mbar_arrive(&empty[(kstage + 2 * t) % F::kStages]);
+                        if (j > 0) mbar_arrive(&vempty[(vbuf + (dual ? 0 : t - 1) + (dual ? half : 0)) & 1]);
+                    }
                     if (!any_live) {  // what the tensor memory holds for these rows goes nowhere
                         if (lane < 2) mbar_arrive(&pfull[2 * half + lane]);
                         continue;
@@ -787,8 +810,12 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 mbar_wait(&ofull[half], ophase, abort_flag, status);
                 ophase ^= 1;
+                if (releases && (dual || half == 1)) mbar_arrive(&vempty[(vbuf + (dual ? half : n - 1)) & 1]);
                 tc_fence_after_sync();
             }
+            const int tiles = sg->t1 - sg->t0;
+            kstage = (kstage + 2 * tiles) % F::kStages;
+            vbuf = (vbuf + tiles) & 1;
 
             float *b_max = reinterpret_cast<float *>(smem + F::kRowOff), *b_sum = b_max + kHalfRows;
             float4 *b_out = reinterpret_cast<float4 *>(smem);  // [32 groups of 4 channels][128 rows]
