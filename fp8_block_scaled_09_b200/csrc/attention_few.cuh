@@ -139,6 +139,24 @@ __device__ __forceinline__ float warp_max(float x) {
     return y;
 }
 
+// Eight BF16 values times `up` (a power of two that takes them below 256) as two
+// E4M3 parts: hi keeps the top 4 of their 8 significant bits, lo the other 4.
+// Both are exact but below 2^-6, where hi is 0 and lo rounds to steps of 2^-9.
+__device__ __forceinline__ void split8(uint4 v, float up, uint2 &hi, uint2 &lo) {
+    float x[8], h[8];
+    unpack_bf16x8(v, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        x[k] *= up;
+        h[k] = fabsf(x[k]) < 0x1p-6f ? 0.0f : __uint_as_float(__float_as_uint(x[k]) & 0xFFF00000u);
+        x[k] -= h[k];
+    }
+    hi = make_uint2(e4m3x2_satfinite(h[0], h[1]) | (static_cast<uint32_t>(e4m3x2_satfinite(h[2], h[3])) << 16),
+                    e4m3x2_satfinite(h[4], h[5]) | (static_cast<uint32_t>(e4m3x2_satfinite(h[6], h[7])) << 16));
+    lo = make_uint2(e4m3x2_satfinite(x[0], x[1]) | (static_cast<uint32_t>(e4m3x2_satfinite(x[2], x[3])) << 16),
+                    e4m3x2_satfinite(x[4], x[5]) | (static_cast<uint32_t>(e4m3x2_satfinite(x[6], x[7])) << 16));
+}
+
 // Two E4M3 codes -> two floats (exact).
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
     uint32_t h2;
@@ -536,22 +554,12 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // power of two that takes the largest channel to [128, 256)
                 const int e = max(static_cast<int>(m >> 7) - 127, -100);
                 const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
-                float f[8];
-                unpack_bf16x8(u, f);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = f[2 * k] * up, y = f[2 * k + 1] * up;
-                    const uint16_t h = e4m3x2_satfinite(x, y);
-                    const float2 d = e4m3x2_to_float2(h);
-                    hi[k] = h;
-                    lo[k] = e4m3x2_satfinite(x - d.x, y - d.y);
-                }
+                uint2 hi, lo;
+                split8(u, up, hi, lo);
                 // rows r and NR + r have the same place in their 8-row swizzle group
                 const int off = r * kDim + (((sub >> 1) ^ (r & 7)) << 4) + (sub & 1) * 8;
-                *reinterpret_cast<uint2 *>(dst + off) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-                *reinterpret_cast<uint2 *>(dst + NR * kDim + off) =
-                    make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+                *reinterpret_cast<uint2 *>(dst + off) = hi;
+                *reinterpret_cast<uint2 *>(dst + NR * kDim + off) = lo;
                 if (sub == 0) {
                     row_scale[rb + r] =
                         a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);

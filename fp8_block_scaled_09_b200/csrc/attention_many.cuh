@@ -47,7 +47,7 @@ constexpr int kSoftmaxRegs = 184, kConvertRegs = 56, kIssueRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <=
                   kManyThreads * kManyLaunchRegs,
               "register split exceeds the launch allocation");
-constexpr int kItemCost = 3;      // tiles' worth of work that an item adds
+constexpr int kItemCost = 5;      // tiles' worth of work that an item adds
 constexpr int kManyMaxGrid = 160;
 constexpr int kHalfRows = 128;
 constexpr float kRescaleAt = 8.0f;  // log2
@@ -711,25 +711,12 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const uint4 pair[2] = {u[0], u[1]};
 #pragma unroll
                     for (int k = 0; k < 14; ++k) u[k] = u[k + 2];
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int d = 0; d < 2; ++d) {
-                        float f[8];
-                        unpack_bf16x8(pair[d], f);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float x0 = f[4 * k] * up, x1 = f[4 * k + 1] * up;
-                            const float x2 = f[4 * k + 2] * up, x3 = f[4 * k + 3] * up;
-                            const uint16_t h0 = e4m3x2_satfinite(x0, x1), h1 = e4m3x2_satfinite(x2, x3);
-                            const float2 d0 = e4m3x2_to_float2(h0), d1 = e4m3x2_to_float2(h1);
-                            hi[2 * d + k] = h0 | (static_cast<uint32_t>(h1) << 16);
-                            lo[2 * d + k] = e4m3x2_satfinite(x0 - d0.x, x1 - d0.y) |
-                                            (static_cast<uint32_t>(e4m3x2_satfinite(x2 - d1.x, x3 - d1.y)) << 16);
-                        }
-                    }
+                    uint2 hi[2], lo[2];
+                    split8(pair[0], up, hi[0], lo[0]);
+                    split8(pair[1], up, hi[1], lo[1]);
                     const int off = (c ^ (ht & 7)) << 4;
-                    *reinterpret_cast<uint4 *>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(dst + F::kQPart + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(dst + off) = make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
+                    *reinterpret_cast<uint4 *>(dst + F::kQPart + off) = make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
