@@ -668,6 +668,11 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
         for (int b = blockIdx.x * 256 + threadIdx.x; b < a.B; b += gridDim.x * 256)
             if (seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
 
+        // 16 bytes number c of a 256-byte row of this warp, in the places of the row's query parts
+        auto staged = [&](int row, int c) {
+            return reinterpret_cast<uint4 *>(smem + (2 * half + (c >> 3)) * F::kQPart +
+                                             ((warp & 3) * 32 + row) * kDim + (((c & 7) ^ (row & 7)) << 4));
+        };
         uint32_t sphase = 0, ophase = 0;
         uint32_t kstage = 0, vbuf = 0;  // of the segment's first tile
         // K and V are released here, by one warp of the half that used a tile last
@@ -691,32 +696,49 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (n > 0) {
                 // the row's query: power of two that takes its largest channel to
                 // [128, 256), two E4M3 parts, K-major with the 128-byte swizzle
-                uint4 u[16];
+                // The warp fetches two rows at a time (a thread its own row would touch 32
+                // lines with each load) and hands them out through the rows' own places
+                // in shared memory.
+                // (This runs once per segment, from instructions that are no longer in the
+                // cache: short loops, since each new line of code costs more than its work.)
+                const int64_t at = live ? q_row * a.q_stride + static_cast<int64_t>(head) * kDim : -1;
+#pragma unroll 1
+                for (int i = 0; i < 16; ++i) {
+                    const int64_t from = __shfl_sync(0xFFFFFFFFu, at, 2 * i + (lane >> 4));
+                    cp_async_16(staged(2 * i + (lane >> 4), lane & 15),
+                                a.q + (from >= 0 ? from : 0) + (lane & 15) * 8, from >= 0 ? 16 : 0);
+                }
+                cp_async_wait_all();
+                __syncwarp();
                 uint32_t top = 0;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    a.q + q_row * a.q_stride + static_cast<int64_t>(head) * kDim);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) u[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) top = max(top, amax_bits8(u[c]));
+#pragma unroll 1
+                for (int c = 0; c < 16; ++c) top = max(top, amax_bits8(*staged(lane, c)));
                 const int e = max(static_cast<int>(top >> 7) - 127, -100);
                 const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
                 const float scale =
                     a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
-                uint8_t *dst = smem + 2 * half * F::kQPart + ht * kDim;
-                // not unrolled (the vectors move down the array instead): the first
-                // pass over the unrolled code fetched it for 5 us
-#pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 pair[2] = {u[0], u[1]};
+                // Parts of 16 channels take the places of their row's 16-byte pieces c and
+                // 8 + c, so the first 8 pieces move to registers and the last go first.
+                uint4 u[8];
 #pragma unroll
-                    for (int k = 0; k < 14; ++k) u[k] = u[k + 2];
+                for (int c = 0; c < 8; ++c) u[c] = *staged(lane, c);
+#pragma unroll 1
+                for (int c = 7; c >= 0; --c) {
+                    uint4 x0, x1;
+                    if (c >= 4) {
+                        x0 = *staged(lane, 2 * c);
+                        x1 = *staged(lane, 2 * c + 1);
+                    } else {
+                        x0 = u[6];
+                        x1 = u[7];
+#pragma unroll
+                        for (int k = 7; k >= 2; --k) u[k] = u[k - 2];
+                    }
                     uint2 hi[2], lo[2];
-                    split8(pair[0], up, hi[0], lo[0]);
-                    split8(pair[1], up, hi[1], lo[1]);
-                    const int off = (c ^ (ht & 7)) << 4;
-                    *reinterpret_cast<uint4 *>(dst + off) = make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
-                    *reinterpret_cast<uint4 *>(dst + F::kQPart + off) = make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
+                    split8(x0, up, hi[0], lo[0]);
+                    split8(x1, up, hi[1], lo[1]);
+                    *staged(lane, c) = make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
+                    *staged(lane, 8 + c) = make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -854,17 +876,34 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     o[4 * k + 3] = fmaf(o[4 * k + 3], f_a, v.w * f_b);
                 }
             };
-            // 32 channels of the output: o times `f` (which takes the 2^8 of V back) in BF16
+            // 32 channels of the output: o times `f` (which takes the 2^8 of V back) in BF16,
+            // to the row's place in shared memory; then all rows of the warp, two at a time.
+            // (Of doubled halves that memory has B's output: they store directly.)
+            uint16_t *out_row = a.out + q_row * a.out_stride + static_cast<int64_t>(head) * kDim;
             auto store = [&](int c, const float *o, float f) {
-                if (!live) return;
-                uint4 *out = reinterpret_cast<uint4 *>(a.out + q_row * a.out_stride + static_cast<int64_t>(head) * kDim) + 4 * c;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float t[8];
 #pragma unroll
                     for (int d = 0; d < 8; ++d) t[d] = f != 0.0f ? o[8 * k + d] * f : 0.0f;
-                    out[k] = pack_bf16x8(t);
+                    const uint4 v = pack_bf16x8(t);
+                    if (!dual)
+                        *staged(lane, 4 * c + k) = v;
+                    else if (live)
+                        reinterpret_cast<uint4 *>(out_row)[4 * c + k] = v;
                 }
+            };
+            auto flush = [&] {
+                if (dual) return;
+                __syncwarp();
+                const int64_t at = live ? out_row - a.out : -1;
+#pragma unroll 2
+                for (int i = 0; i < 16; ++i) {
+                    const int64_t to = __shfl_sync(0xFFFFFFFFu, at, 2 * i + (lane >> 4));
+                    if (to >= 0)
+                        *reinterpret_cast<uint4 *>(a.out + to + (lane & 15) * 8) = *staged(2 * i + (lane >> 4), lane & 15);
+                }
+                __syncwarp();
             };
             auto store_lse = [&](float m, float l) {
                 if (live && a.lse != nullptr)
@@ -879,6 +918,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     output(c, o);
                     store(c, o, f);
                 }
+                flush();
                 store_lse(m_run, l_run);
                 if (dual) named_barrier(3, 256);
                 continue;
@@ -951,6 +991,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 store(c, o, f);
             }
+            flush();
             store_lse(m, l);
         }
     }

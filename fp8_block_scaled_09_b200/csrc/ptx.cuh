@@ -377,6 +377,13 @@ __device__ __forceinline__ void cp_async_4(void *smem_dst, const void *gmem_src)
                  : "memory");
 }
 
+// 16-byte one; the bytes from src_bytes (0 or 16) on are zeros.
+__device__ __forceinline__ void cp_async_16(void *smem_dst, const void *gmem_src, uint32_t src_bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem_dst)),
+                 "l"(gmem_src), "r"(src_bytes)
+                 : "memory");
+}
+
 // Waits for all of this thread's cp.async copies.
 __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_all;" ::: "memory");
