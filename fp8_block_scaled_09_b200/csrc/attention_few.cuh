@@ -1,5 +1,7 @@
-// attention_few.cuh -- paged attention for few query rows per kv head (decode,
-// a short block): q_len * group <= NR rows, NR = 8, 16 or 32.
+// attention_few.cuh -- paged attention for few query rows per kv head (decode):
+// q_len * group <= NR rows, NR = 8 or 16.  (From 17 rows on the other kernel is
+// faster: 28 rows, 16 sequences of 4500 positions, took 63 us here with NR = 32, 47 us
+// there; 14 rows take 37 us here.)
 //
 // Bound by the cache's bytes: 256 per position and kv head, read once.  The
 // E4M3 codes go from HBM to shared memory by TMA and from there straight into
@@ -48,7 +50,7 @@ constexpr int kTile = 128;                 // positions
 constexpr int kStageBytes = kTile * kDim;  // one K or V tile of codes
 constexpr int kFewSoftmaxWarps = 8;
 constexpr int kFewThreads = 32 * (3 + kFewSoftmaxWarps);
-constexpr int kHeadCost = 2;     // tiles' worth of work that a (sequence, head) adds
+constexpr int kHeadCost = 4;     // tiles' worth of work that a (sequence, head) adds
 constexpr float kPScale = 8.0f;  // weights are held times 2^8
 
 template <int NR>
@@ -60,7 +62,7 @@ struct Few {
     // a whole chunk of P, so that the softmax never waits for V; half per group
     static constexpr int kGroupSlots = (kChunk + 1) / 2;
     static constexpr int kPSlots = 2 * kGroupSlots;
-    static constexpr int kStages = NR == 32 ? 10 : 11;
+    static constexpr int kStages = 11;
     static constexpr int kQOff = kStages * kStageBytes;  // [2]
     static constexpr int kPOff = kQOff + 2 * kQ;         // [kPSlots]
     static constexpr int kBarOff = kPOff + kPSlots * kP;
@@ -749,14 +751,11 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_wait(&sfull[buf], (g >> 1) & 1, abort_flag, status);
             tc_fence_after_sync();
 
-            // scores of tile j, rows [c, c + X): hi + lo
+            // scores of tile j: hi + lo
             auto load_scores = [&](int j, auto &v) {
                 float lo[NR];
-#pragma unroll
-                for (int c = 0; c < NR; c += NR < 16 ? NR : 16) {
-                    tmem_ld<NR < 16 ? NR : 16>(tm + F::s_col(buf, j) + c, v + c);
-                    tmem_ld<NR < 16 ? NR : 16>(tm + F::s_col(buf, j) + NR + c, lo + c);
-                }
+                tmem_ld<NR>(tm + F::s_col(buf, j), v);
+                tmem_ld<NR>(tm + F::s_col(buf, j) + NR, lo);
                 tmem_ld_wait<NR>(v);
                 tmem_ld_wait<NR>(lo);
 #pragma unroll
@@ -831,11 +830,8 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if constexpr (NR == 8) {
                     *p = make_uint4(hi[0], hi[1], lo[0], lo[1]);
                 } else {
-#pragma unroll
-                    for (int c = 0; c < NR / 16; ++c) {
-                        p[c * kTile] = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-                        p[(NR / 16 + c) * kTile] = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-                    }
+                    p[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    p[kTile] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 if ((cur.t + j + 1) * kTile > len) {
                     // the tile in which the sequence ends: what its page holds behind the

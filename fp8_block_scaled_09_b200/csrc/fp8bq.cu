@@ -25,8 +25,8 @@
 //                       smaller M: the decode GEMM, then silu_mul_quantize
 //   rms_norm_quantize -> rms_norm_kernel<V> (one CTA per row, V vectors per thread)
 //   rope_kv_write_e4m3 -> rope_kv_write_kernel
-//   paged_attention  -> up to 32 query rows (new tokens x heads of a group) per kv head:
-//                       attn::attention_few_kernel<8|16|32> (rows are the MMA's columns);
+//   paged_attention  -> up to 16 query rows (new tokens x heads of a group) per kv head:
+//                       attn::attention_few_kernel<8|16> (rows are the MMA's columns);
 //                       more: attn::attention_many_kernel (256 rows per CTA)
 //   linear           -> quantize_act into the workspace, then the gemm path; the
 //                       decode kernel then streams its first weight blocks while
@@ -249,8 +249,6 @@ const DeviceInfo *device_info() {
             return;
         if (cudaFuncSetAttribute(attn::attention_few_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  attn::Few<16>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(attn::attention_few_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 attn::Few<32>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(attn::attention_few_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  attn::Few<8>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(attn::attention_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -734,7 +732,7 @@ size_t few_ws_bytes() {
 
 size_t attention_ws_bytes(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_q_len) {
     const int64_t rows = attention_rows(T, q_heads, kv_heads, max_q_len);
-    return rows <= 8 ? few_ws_bytes<8>() : rows <= 16 ? few_ws_bytes<16>() : rows <= 32 ? few_ws_bytes<32>() : kManyWsBytes;
+    return rows <= 8 ? few_ws_bytes<8>() : rows <= 16 ? few_ws_bytes<16>() : kManyWsBytes;
 }
 
 template <int NR>
@@ -765,7 +763,6 @@ fp8bq_status launch_attention(const DeviceInfo &d, const attn::Args &a, int64_t 
     const int64_t rows = int64_t(a.max_q) * a.group;
     if (rows <= 8) return from_cuda(launch_few<8>(d, a, tk, tv, ws, st));
     if (rows <= 16) return from_cuda(launch_few<16>(d, a, tk, tv, ws, st));
-    if (rows <= 32) return from_cuda(launch_few<32>(d, a, tk, tv, ws, st));
     const int grid = std::min<int>(d.sm_count, attn::kManyMaxGrid);
     return from_cuda(launch(attn::attention_many_kernel, dim3(static_cast<unsigned>(grid)),
                             dim3(attn::kManyThreads), attn::Many::kBytes, st, tk, tv, a,
