@@ -36,7 +36,8 @@
 // Roles: warp 0 TMA producer (a page per lane), warp 1 MMA issuer, warps 2..9
 // softmax (two groups of four that take a chunk's tiles in turn; thread = one
 // position of the tile, its TMEM lane, in the score phase, one output channel
-// of half the rows in the merge), warp 10 queries.
+// of half the rows in the merge), warp 10 queries, warp 11 follows the ring and clears
+// V behind a sequence's end.
 #pragma once
 
 #include "attention.cuh"
@@ -49,7 +50,7 @@ namespace attn {
 constexpr int kTile = 128;                 // positions
 constexpr int kStageBytes = kTile * kDim;  // one K or V tile of codes
 constexpr int kFewSoftmaxWarps = 8;
-constexpr int kFewThreads = 32 * (3 + kFewSoftmaxWarps);
+constexpr int kFewThreads = 32 * (4 + kFewSoftmaxWarps);
 constexpr int kHeadCost = 4;     // tiles' worth of work that a (sequence, head) adds
 constexpr float kPScale = 8.0f;  // weights are held times 2^8
 
@@ -66,8 +67,8 @@ struct Few {
     static constexpr int kQOff = kStages * kStageBytes;  // [2]
     static constexpr int kPOff = kQOff + 2 * kQ;         // [kPSlots]
     static constexpr int kBarOff = kPOff + kPSlots * kP;
-    // full, empty; pfull, pempty; qfull (4), qempty, sfull, sfree, ofull, ofree, vready (2 each)
-    static constexpr int kBars = 2 * kStages + 2 * kPSlots + 4 + 12;
+    // full, empty, cleared; pfull, pempty; qfull (4), qempty, sfull, sfree, ofull, ofree (2 each)
+    static constexpr int kBars = 3 * kStages + 2 * kPSlots + 4 + 10;
     // per-row values: scale and limit [4], maximum and factor [2], negated maximum,
     // reductions over the warps [8], sums over the warps [2][8]
     static constexpr int kRowOff = kBarOff + kBars * 8;
@@ -272,8 +273,9 @@ struct Chunks {
                 tiles = seq_tiles(seq);
             }
             const int cost = static_cast<int>(head_cost(tiles));
-            const int rel = static_cast<int>((w - base) % cost);
-            hk = static_cast<int>((w - base) / cost);
+            const uint32_t off = static_cast<uint32_t>(w - base);  // the host bounds cost * kv_heads
+            hk = static_cast<int>(off / static_cast<uint32_t>(cost));
+            const int rel = static_cast<int>(off - static_cast<uint32_t>(hk) * cost);
             const int64_t left = min(static_cast<int64_t>(cost - rel), w_end - w);
             t = seg_t0 = max(rel - kHeadCost, 0);
             seg_end = max(static_cast<int>(rel + left) - kHeadCost, 0);
@@ -306,7 +308,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
     uint64_t *pfull = empty + F::kStages;
     uint64_t *pempty = pfull + F::kPSlots;
     uint64_t *qfull = pempty + F::kPSlots, *qempty = qfull + 4, *sfull = qempty + 2,
-             *sfree = sfull + 2, *ofull = sfree + 2, *ofree = ofull + 2, *vready = ofree + 2;
+             *sfree = sfull + 2, *ofull = sfree + 2, *ofree = ofull + 2, *cleared = ofree + 2;
     float *row_scale = reinterpret_cast<float *>(smem + F::kRowOff);  // [4] score -> log2 weight
     int *row_lim = reinterpret_cast<int *>(row_scale + 4 * NR);       // [4] last position seen
     float *row_max = reinterpret_cast<float *>(row_lim + 4 * NR);     // [2] maximum (log2), by chunk
@@ -327,7 +329,8 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], 2);
+            mbar_init(&cleared[i], 1);
         }
         for (int i = 0; i < F::kPSlots; ++i) {
             mbar_init(&pfull[i], 4);
@@ -340,7 +343,6 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(&sfree[i], kFewSoftmaxWarps);
             mbar_init(&ofull[i], 1);
             mbar_init(&ofree[i], kFewSoftmaxWarps);
-            mbar_init(&vready[i], 1);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -444,6 +446,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
         uint32_t stage = 0, phase = 0;
         uint32_t pslot[2] = {0, 0}, pphase[2] = {0, 0};  // of each softmax group
         uint32_t gk = 0, gv = 0, segs = 0;  // chunks and segments so far
+        uint32_t cphases = 0;               // bit i: phase of cleared[i]
         bool ok = true;
         auto advance = [&] {
             if (++stage == F::kStages) {
@@ -492,9 +495,12 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             for (int j = 0; j < cur.n && ok; ++j) {
                 const int h = j & 1;
                 const uint32_t slot = h * F::kGroupSlots + pslot[h];
-                wait(&full[stage], phase);
-                // the sequence ends in this tile: its softmax group clears what is behind
-                if (ok && (cur.t + j + 1) * kTile > cur.seq.len && lane == 0) mbar_arrive(&vready[h]);
+                if ((cur.t + j + 1) * kTile > cur.seq.len) {
+                    wait(&cleared[stage], (cphases >> stage) & 1);
+                    cphases ^= 1u << stage;
+                } else {
+                    wait(&full[stage], phase);
+                }
                 wait(&pfull[slot], pphase[h]);
                 if (!ok) break;
                 tc_fence_after_sync();
@@ -575,6 +581,41 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (lane == 0) mbar_arrive(&qfull[segs & 3]);
             ++segs;
         }
+    } else if (warp == 3 + kFewSoftmaxWarps) {
+        // ------------------------------------------------------------ ends of sequences
+        // What a page holds behind the end of its sequence may be NaN, which a
+        // weight of 0 would not silence: those rows of V become zeros as soon as they are
+        // there.  This warp takes part in every slot's release, so that it sees each
+        // of the ring's tiles.
+        Chunks<NR> ahead = cur;
+        bool more = ahead.next();
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        auto follow = [&](const Chunks<NR> &c, bool v) {
+            for (int t = c.t; t < c.t + c.n && ok; ++t) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, abort_flag, status));
+                if (!ok) return;
+                const int from = c.seq.len - t * kTile;  // first row behind the end
+                if (v && from < kTile) {
+                    uint4 *z = reinterpret_cast<uint4 *>(smem + stage * kStageBytes);
+                    for (int i = from * 8 + lane; i < kTile * 8; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&cleared[stage]);
+                }
+                if (lane == 0) mbar_arrive(&empty[stage]);
+                if (++stage == F::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        };
+        if (more) follow(ahead, false);
+        while (ok && cur.next()) {
+            more = ahead.next();
+            if (more) follow(ahead, false);
+            follow(cur, true);
+        }
     } else {
         // ------------------------------------------------------------ softmax
         // A wait that gives up sets the abort flag: the loops then run to their
@@ -603,11 +644,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
         float l_run[NR];     // sums over this thread's positions
         float o_run[kHalf];  // this thread's channel of rows group * kHalf ...
-        uint32_t g = 0, segs = 0, pslot = 0, pphase = 0, ragged = 0;
-        uint32_t vstage = 0;  // ring stage of the next V tile
-        Chunks<NR> ahead = cur;
-        bool more = ahead.next();
-        if (more) vstage = ahead.n % F::kStages;
+        uint32_t g = 0, segs = 0, pslot = 0, pphase = 0;
         // what the merge and the end of a segment need of the chunk before
         struct {
             int q0, hk, rows, tiles, seg_t0, seg_end;
@@ -736,8 +773,6 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
         };
 
         while (cur.next()) {
-            more = ahead.next();
-            if (more) vstage = (vstage + ahead.n) % F::kStages;  // V of this chunk follows K of the next
             const uint32_t buf = g & 1;
             const int rows = cur.seq.q_len * G, len = cur.seq.len;
             if (cur.first) {
@@ -833,16 +868,6 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     p[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     p[kTile] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                if ((cur.t + j + 1) * kTile > len) {
-                    // the tile in which the sequence ends: what its page holds behind the
-                    // end may be NaN, which a weight of 0 would not silence
-                    mbar_wait(&vready[group], ragged++ & 1, abort_flag, status);
-                    if (pos >= len) {
-                        uint4 *z = reinterpret_cast<uint4 *>(smem + (vstage + j) % F::kStages * kStageBytes + lane_row * kDim);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) z[k] = make_uint4(0, 0, 0, 0);
-                    }
-                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pfull[slot]);
@@ -854,7 +879,6 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sfree[buf]);
-            vstage = (vstage + cur.n) % F::kStages;
             if (cur.last) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {

@@ -219,8 +219,9 @@ struct Items {
                 }
                 cost = tiles_until(a, seq, m * 256 + 256) + kItemCost;
             }
-            const int rel = static_cast<int>((w - base) % cost);
-            hk = static_cast<int>((w - base) / cost);
+            const uint32_t off = static_cast<uint32_t>(w - base);  // the host bounds cost * kv_heads
+            hk = static_cast<int>(off / static_cast<uint32_t>(cost));
+            const int rel = static_cast<int>(off - static_cast<uint32_t>(hk) * cost);
             const int64_t left = min(static_cast<int64_t>(cost - rel), w_end - w);
             t0 = max(rel - kItemCost, 0);
             t1 = max(static_cast<int>(rel + left) - kItemCost, 0);

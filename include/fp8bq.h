@@ -329,7 +329,8 @@ FP8BQ_API fp8bq_status fp8bq_rope_kv_write_e4m3(
  *                      kv_heads, max_q_len) bytes, same state rule as fp8bq_gemm
  *                      (one workspace may serve both, in stream order)
  * Heads have 128 channels; q_heads a multiple of kv_heads, at most 1024;
- * page_size a power of two from 8 to 2^20, max_pages * page_size <= 2^30;
+ * page_size a power of two from 8 to 2^20, max_pages * page_size <= 2^30 (2^37 over
+ * all kv heads);
  * B <= 65536, T < 2^21; scale > 0; q, out and the caches 16-byte aligned,
  * q_stride and out_stride multiples of 8, slot_stride of 16.
  * Slots at or behind a sequence's length may hold anything, NaN codes too;
