@@ -20,8 +20,8 @@
 // as many of them the tensor pipe was busy 1100 of 2550 cycles per tile.)
 //
 // Work is a list of tiles of 128 positions, ordered by (sequence, kv head,
-// tile), each head preceded by kHeadCost tiles' worth of nothing for what
-// beginning and ending it costs; CTA c of a grid of one CTA per SM takes the
+// tile), each head preceded by some tiles' worth of nothing for what
+// beginning and ending it costs (head_cost); CTA c of a grid of one CTA per SM takes the
 // c-th equal part, whatever the sequences' lengths.  A part's tiles of one
 // (sequence, head), its segment, are taken in chunks of at most kChunk tiles,
 // as many as TMEM holds scores for (twice): a chunk's scores are all there
@@ -51,7 +51,6 @@ constexpr int kTile = 128;                 // positions
 constexpr int kStageBytes = kTile * kDim;  // one K or V tile of codes
 constexpr int kFewSoftmaxWarps = 8;
 constexpr int kFewThreads = 32 * (4 + kFewSoftmaxWarps);
-constexpr int kHeadCost = 4;     // tiles' worth of work that a (sequence, head) adds
 constexpr float kPScale = 8.0f;  // weights are held times 2^8
 
 template <int NR>
@@ -237,9 +236,13 @@ struct PageWalk {
     }
 };
 
-// Positions of the work list that one head of a sequence takes.
-__device__ __forceinline__ int64_t head_cost(int tiles) {
-    return tiles > 0 ? static_cast<int64_t>(tiles) + kHeadCost : 0;
+// Positions of the work list that one head of a sequence takes: its tiles and what
+// beginning and ending it costs, about 4 us -- 4 tiles, or 2 with small pages, whose
+// tiles take longer (128 sequences of 1 .. 4096 positions, pages of 64: 164 us at 2,
+// 132 at 4, 127 at 5; pages of 16: 150 us at 2, 154 at 3, 156 at 4).
+__device__ __forceinline__ int head_extra(const Args &a) { return a.page_shift < 5 ? 2 : 4; }
+__device__ __forceinline__ int64_t head_cost(const Args &a, int tiles) {
+    return tiles > 0 ? static_cast<int64_t>(tiles) + head_extra(a) : 0;
 }
 
 // The chunks of one CTA's part of the work list, in order.
@@ -267,18 +270,18 @@ struct Chunks {
         while (t >= seg_end) {  // a new segment
             n = 0;
             if (w >= w_end) return false;
-            while (w >= base + head_cost(tiles) * a.kv_heads) {
-                base += head_cost(tiles) * a.kv_heads;
+            while (w >= base + head_cost(a, tiles) * a.kv_heads) {
+                base += head_cost(a, tiles) * a.kv_heads;
                 seq = seq_of(a, ++b);
                 tiles = seq_tiles(seq);
             }
-            const int cost = static_cast<int>(head_cost(tiles));
+            const int cost = static_cast<int>(head_cost(a, tiles));
             const uint32_t off = static_cast<uint32_t>(w - base);  // the host bounds cost * kv_heads
             hk = static_cast<int>(off / static_cast<uint32_t>(cost));
             const int rel = static_cast<int>(off - static_cast<uint32_t>(hk) * cost);
             const int64_t left = min(static_cast<int64_t>(cost - rel), w_end - w);
-            t = seg_t0 = max(rel - kHeadCost, 0);
-            seg_end = max(static_cast<int>(rel + left) - kHeadCost, 0);
+            t = seg_t0 = max(rel - head_extra(a), 0);
+            seg_end = max(static_cast<int>(rel + left) - head_extra(a), 0);
             w += left;
         }
         first = t == seg_t0;
@@ -290,7 +293,7 @@ struct Chunks {
         return true;
     }
     // the list's position of the current (sequence, head)'s first tile
-    __device__ int64_t item() const { return base + hk * head_cost(tiles) + kHeadCost; }
+    __device__ int64_t item() const { return base + hk * head_cost(a, tiles) + head_extra(a); }
 };
 
 template <int NR>
@@ -359,7 +362,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // run of sequences, then the lane whose run holds the first position finds it
         const int per = (a.B + 31) / 32, b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
         int64_t mine = 0;
-        for (int b = b0; b < b1; ++b) mine += head_cost(seq_tiles(seq_of(a, b)));
+        for (int b = b0; b < b1; ++b) mine += head_cost(a, seq_tiles(seq_of(a, b)));
         mine *= a.kv_heads;
         int64_t incl = mine;
 #pragma unroll
@@ -375,7 +378,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             int64_t base = incl - mine;
             int b = b0;
             for (;; ++b) {
-                const int64_t n = head_cost(seq_tiles(seq_of(a, b))) * a.kv_heads;
+                const int64_t n = head_cost(a, seq_tiles(seq_of(a, b))) * a.kv_heads;
                 if (w0 < base + n) break;
                 base += n;
             }
