@@ -44,10 +44,11 @@ def attention(q, k_cache, v_cache, table, seq_lens, cu_q, page, q_heads, kv_head
     """(out, lse, bound, lse_bound): float64 [T, q_heads, 128], [T, q_heads], and error bounds of both.
 
     The bound: half a BF16 step of the output, plus what the weights may be off by.  A weight
-    is off by 2^-10 of itself (rounded to at least 11 bits, or to two E4M3 parts of 4 bits, and
-    an exponential of a few FP32 ulps), by 2^-17 of the row's largest (the two-part rounding's
-    absolute floor), and by twice the error of its exponent: q may be held in two E4M3 parts
-    (off by 2^-17 of its row's largest channel) and 128 products are summed in FP32.
+    is off by 2^-8 of itself (in two E4M3 parts: the first is within 2^-4, the second within 2^-4
+    of the rest; in F16 it is 2^-11; an exponential's few FP32 ulps are far below), by 2^-17 of the
+    row's largest (the absolute floor of two parts, 2^-10 of 256, and of the sum), and by twice the
+    error of its exponent: q may be held in two E4M3 parts (off by 2^-17 of its row's largest
+    channel) and 128 products are summed in FP32.
 
     lse: every exponent is off by that dz at most, so log sum exp(z + e), |e| <= dz, is off by dz at
     most (each term changes by a factor within exp(+-dz)).  dz is relative to the sum of the
@@ -82,7 +83,7 @@ def attention(q, k_cache, v_cache, table, seq_lens, cu_q, page, q_heads, kv_head
                 dz = scale * (2.0 ** -17 * x.abs().amax(1) * k.abs().sum(1).max() +
                               128 * 2.0 ** -23 * (x.abs() @ k.abs().T).amax(1))
                 lse_bound[cu[b]:cu[b + 1], h] = dz + 2.0 ** -16 + 2.0 ** -21 * torch.where(torch.isinf(l), 0.0, l.abs())
-                off = (w * (2.0 ** -10 + 2 * dz[:, None])) @ v.abs()
+                off = (w * (2.0 ** -8 + 2 * dz[:, None])) @ v.abs()
                 off += 2.0 ** -17 * w.amax(1, keepdim=True) * ((w > 0).double() @ v.abs())
                 out[cu[b]:cu[b + 1], h] = o
                 bound[cu[b]:cu[b + 1], h] = HALF_BF16 * o.abs() + off + 1e-30
