@@ -5,11 +5,13 @@
 // channels, (a, b) = (x[j], x[j + rot/2]) or, interleaved, (x[2j], x[2j + 1]):
 //     (a', b') = m (a cos u - b sin u,  b cos u + a sin u),  u = p inv_freq[j].
 // The angle of a far position needs more than FP32 (p f has up to 55 bits, and
-// an error of 2^-24 of 10^6 radians would be 0.06): p f / 2 pi is formed in
-// FP64, reduced to its fraction, and only that goes to the FP32 sine and
-// cosine.  The rotation is FP32; queries are rounded once to BF16, keys once
-// to E4M3 (not through BF16, which would round them twice), values as the
-// plain cache write does.
+// an error of 2^-24 of 10^6 radians would be 0.06): p f / 2 pi is formed and
+// reduced to its fraction in FP64, and so are sine and cosine, once per token
+// and pair and rounded once with m (FP32 ones cost the same time, 59 us for the
+// 8192 tokens below, and put 3 times as many keys on the other side of a tie).
+// The rotation is FP32; queries are rounded once to BF16, keys once to E4M3 (not
+// through BF16, which would round them twice), values as the plain cache write
+// does.
 //
 // HBM-bound: 2 bytes read per channel, 2 written per query channel, 1 per key
 // or value channel.  `span` threads take a token: thread (j, g) the 16 channels
@@ -85,9 +87,9 @@ rope_kv_write_kernel(const RopeArgs a, int *status) {
         const int t = i / pairs, k = i - t * pairs;
         const double turns = static_cast<double>(a.positions[t0 + t]) *
                              static_cast<double>(__ldg(a.inv_freq + k)) * 0.15915494309189533577;
-        float c, s;
-        sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
-        cs[t][k] = make_float2(c * a.mscale, s * a.mscale);
+        double c, s;
+        sincospi(2.0 * (turns - rint(turns)), &s, &c);
+        cs[t][k] = make_float2(static_cast<float>(c * a.mscale), static_cast<float>(s * a.mscale));
     }
     const int64_t slot = mine ? a.loc[t0 + tok] : -1;
     if (in == 0 && mine && (slot < -1 || slot >= a.num_slots)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
