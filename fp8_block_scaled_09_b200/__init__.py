@@ -420,42 +420,37 @@ def _dense(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int, name: st
     _refuse(t, dtype, shape, dev, name)
 
 
-def _rows(t: torch.Tensor, cols: int, rows: int, dev: int, name: str) -> tuple[int, int]:
-    """Pointer and row stride of a BF16 [rows, cols] tensor with unit column stride."""
-    if t.dtype is torch.bfloat16 and t.shape == (rows, cols) and t.get_device() == dev:
-        step, unit = t.stride()
-        if rows > 1 and unit == 1:
-            return t.data_ptr(), step
-        if rows <= 1 and (unit == 1 or cols <= 1):
-            return t.data_ptr(), max(step, cols)
+def _rows(t: torch.Tensor, cols: int, rows: int, dev: int, name: str) -> int:
+    """Row stride of a BF16 [rows, cols] tensor with unit column stride."""
+    if t.dtype is not torch.bfloat16 or t.shape != (rows, cols) or t.get_device() != dev:
+        _refuse(t, torch.bfloat16, (rows, cols), dev, name)
+    step, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    _refuse(t, torch.bfloat16, (rows, cols), dev, name)
+    return step if rows > 1 else max(step, cols)
 
 
 def _first(t: torch.Tensor, name: str) -> int:
-    """The device of a call, from its first tensor: BF16, two dimensions."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    return t.get_device()
+    """The device of a call, from its first tensor: on a GPU, two dimensions."""
+    dev = t.get_device()
+    if dev < 0 or t.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA tensor of two dimensions, got {tuple(t.shape)} on {t.device}")
+    return dev
 
 
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_stream_of = _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _call(t: torch.Tensor, dev: int, name: str, *args) -> None:
-    """Calls the library on t's device and its current stream (passed as the last argument)."""
-    f = getattr(lib(), name)
+def _call(dev: int, f, *args) -> None:
+    """Calls a library function with this device current and its current stream as the last argument."""
     if dev == _get_device():
-        status = f(*args, _stream(t))
+        status = f(*args, _stream_of(dev))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, _stream(t))
+            status = f(*args, _stream_of(dev))
     if status != 0:
-        raise Fp8bqError(status, name)
+        raise Fp8bqError(status, f.__name__)
 
 
 def _norm(x, weight, eps, residual, residual_out, q, s, h) -> None:
@@ -476,7 +471,7 @@ def _norm(x, weight, eps, residual, residual_out, q, s, h) -> None:
         pq = _dense(_codes(q), torch.uint8, shape, dev, "q")
         ps = _dense(s, torch.float32, (M, K // 128), dev, "s")
     ph = None if h is None else _dense(h, torch.bfloat16, shape, dev, "h")
-    _call(x, dev, "fp8bq_rms_norm_quantize", px, pr, pw, eps, M, K, po, pq, ps, ph)
+    _call(dev, (_lib or lib()).fp8bq_rms_norm_quantize, px, pr, pw, eps, M, K, po, pq, ps, ph)
 
 
 def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
@@ -530,8 +525,12 @@ def _caches(k_cache, v_cache, dev) -> tuple[int, int, int, int]:
     shape = k_cache.shape
     if len(shape) != 2:
         raise ValueError("k_cache and v_cache must be [num_slots, slot_bytes]")
-    return (_dense(_codes(k_cache), torch.uint8, shape, dev, "k_cache"),
-            _dense(_codes(v_cache), torch.uint8, shape, dev, "v_cache"), shape[0], shape[1])
+    if k_cache.dtype is not torch.uint8:
+        k_cache = _codes(k_cache)
+    if v_cache.dtype is not torch.uint8:
+        v_cache = _codes(v_cache)
+    return (_dense(k_cache, torch.uint8, shape, dev, "k_cache"),
+            _dense(v_cache, torch.uint8, shape, dev, "v_cache"), shape[0], shape[1])
 
 
 def rope_kv_write_e4m3(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -547,7 +546,7 @@ def rope_kv_write_e4m3(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: tor
     qkv's own query columns)."""
     dev = _first(qkv, "qkv")
     T, cols = qkv.shape
-    px, step = _rows(qkv, cols, T, dev, "qkv")
+    step = _rows(qkv, cols, T, dev, "qkv")
     pk, pv, slots, slot_bytes = _caches(k_cache, v_cache, dev)
     if head_dim <= 0 or cols % head_dim:
         raise ValueError("qkv columns must be a multiple of head_dim")
@@ -564,9 +563,10 @@ def rope_kv_write_e4m3(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: tor
     pf = _dense(inv_freq, torch.float32, (pairs,), dev, "inv_freq")
     if q_out is None:
         q_out = torch.empty((T, q_heads * head_dim), dtype=torch.bfloat16, device=qkv.device)
-    po, out_step = _rows(q_out, q_heads * head_dim, T, dev, "q_out")
-    _call(qkv, dev, "fp8bq_rope_kv_write_e4m3", px, step, T, q_heads, kv_heads, head_dim, pp, pf,
-          2 * pairs, 1 if interleaved else 0, mscale, pl, po, out_step, pk, pv, slots, slot_bytes)
+    out_step = _rows(q_out, q_heads * head_dim, T, dev, "q_out")
+    _call(dev, (_lib or lib()).fp8bq_rope_kv_write_e4m3, qkv.data_ptr(), step, T, q_heads, kv_heads,
+          head_dim, pp, pf, 2 * pairs, 1 if interleaved else 0, mscale, pl, q_out.data_ptr(), out_step,
+          pk, pv, slots, slot_bytes)
     return q_out
 
 
@@ -596,7 +596,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     pages and lengths are reported through last_device_status()."""
     dev = _first(q, "q")
     T, width = q.shape[0], q_heads * HEAD_DIM
-    pq, step = _rows(q, width, T, dev, "q")
+    step = _rows(q, width, T, dev, "q")
     pk, pv, slots, slot_bytes = _caches(k_cache, v_cache, dev)
     if page_table.dtype is not torch.int32 or page_table.dim() != 2:
         raise TypeError("page_table must be int32 [B, max_pages]")
@@ -610,13 +610,13 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     pc = _dense(cu_q, torch.int32, (B + 1,), dev, "cu_q")
     if out is None:
         out = torch.empty((T, width), dtype=torch.bfloat16, device=q.device)
-    po, out_step = _rows(out, width, T, dev, "out")
+    out_step = _rows(out, width, T, dev, "out")
     pe = None if lse is None else _dense(lse, torch.float32, (T, q_heads), dev, "lse")
     if workspace is None:
         workspace = new_attention_workspace(T, B, q_heads, kv_heads, max_q_len, q.device)
     pw = _dense(workspace, torch.uint8, workspace.shape, dev, "workspace")
-    _call(q, dev, "fp8bq_paged_attention", pq, step, pk, pv, slots, slot_bytes,
+    _call(dev, (_lib or lib()).fp8bq_paged_attention, q.data_ptr(), step, pk, pv, slots, slot_bytes,
           page_table.data_ptr(), table_step if B > 1 else max(pages, table_step), pages, page_size,
           pl, pc, B, T, q_heads, kv_heads, max_q_len, HEAD_DIM ** -0.5 if scale is None else scale,
-          1 if causal else 0, po, out_step, pe, pw, workspace.numel())
+          1 if causal else 0, out.data_ptr(), out_step, pe, pw, workspace.numel())
     return out

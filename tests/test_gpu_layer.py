@@ -150,3 +150,37 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for (_, alone), got in zip(runs, outs):
         assert all(torch.equal(alone, o) for o in got)
+
+
+def test_binding_refuses_wrong_tensors():
+    """Types, shapes, layouts and devices that do not fit are refused before anything runs."""
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    x, w = b(4, 256), b(256)
+    before = fp8bq.launch_count()
+    for bad in (dict(x=x.float()), dict(x=x[0]), dict(x=b(4, 512)[:, ::2]), dict(w=b(128)), dict(w=w.cpu()),
+                dict(residual=b(3, 256)), dict(residual_out=x), dict(residual=x, residual_out=b(4, 128)),
+                dict(q=torch.zeros(4, 256, device="cuda")), dict(s=torch.zeros(4, 3, device="cuda")), dict(h=b(4, 255))):
+        a = {"x": x, "w": w, **bad}
+        with pytest.raises((TypeError, ValueError)):
+            fp8bq.rms_norm_quantize(a.pop("x"), a.pop("w"), **a)
+    i64 = torch.arange(4, device="cuda")
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")
+    good = dict(qkv=b(4, 3 * 128), positions=i64, inv_freq=torch.ones(64, device="cuda"), loc=i64, k_cache=u8(8, 128), v_cache=u8(8, 128))
+    for bad in (dict(qkv=b(4, 100)), dict(qkv=b(4, 2 * 128)), dict(positions=i64.int()), dict(positions=i64[:3]),
+                dict(loc=i64.cpu()), dict(inv_freq=torch.ones(2, 32, device="cuda")), dict(v_cache=u8(7, 128)),
+                dict(k_cache=u8(8 * 128)), dict(q_out=b(4, 256)), dict(q_out=b(128, 4).T), dict(head_dim=0)):
+        with pytest.raises((TypeError, ValueError)):
+            fp8bq.rope_kv_write_e4m3(**{**good, **bad})
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    good = dict(q=b(2, 256), k_cache=u8(32, 128), v_cache=u8(32, 128), page_table=i32([0, 1], [1, 0]), seq_lens=i32(5, 6),
+                cu_q=i32(0, 1, 2), page_size=16, q_heads=2, kv_heads=1, max_q_len=1)
+    for bad in (dict(q=b(2, 128)), dict(q=b(256, 2).T), dict(seq_lens=i32(5)), dict(cu_q=i32(0, 1)), dict(cu_q=torch.arange(3, device="cuda")),
+                dict(page_table=i32(0, 1)), dict(page_table=i32([0, 1], [1, 0]).T.contiguous().T), dict(v_cache=u8(16, 128)),
+                dict(out=b(2, 255)), dict(lse=b(2, 2)), dict(lse=torch.zeros(2, 1, device="cuda")), dict(workspace=b(1 << 22)),
+                dict(page_size=24), dict(q_heads=3, q=b(2, 384), kv_heads=2), dict(max_q_len=0), dict(scale=0.0),
+                dict(workspace=u8(256))):
+        with pytest.raises((TypeError, ValueError, fp8bq.Fp8bqError)):
+            fp8bq.paged_attention(**{**good, **bad})
+    assert fp8bq.launch_count() == before
+    fp8bq.paged_attention(**good)
+    assert fp8bq.launch_count() == before + 1
