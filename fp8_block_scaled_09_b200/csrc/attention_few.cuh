@@ -167,7 +167,7 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
 }
 
 // A sequence as the kernels take it: lengths that the host cannot check are
-// clamped (seq_check reports them).
+// clamped (seq_is_bad reports them).
 struct Seq {
     int len;     // cache positions
     int q0;      // first row of q
@@ -181,8 +181,7 @@ __device__ __forceinline__ Seq seq_of(const Args &a, int b) {
     s.len = min(max(__ldg(a.seq_lens + b), 0), cap);
     const int T = static_cast<int>(a.T);
     s.q0 = min(max(__ldg(a.cu_q + b), 0), T);
-    const int q1 = __ldg(a.cu_q + b + 1);
-    s.q_real = max(q1 - s.q0, 0);
+    s.q_real = max(__ldg(a.cu_q + b + 1), s.q0) - s.q0;
     s.q_len = min(min(s.q_real, T - s.q0), a.max_q);
     return s;
 }
@@ -190,7 +189,7 @@ __device__ __forceinline__ Seq seq_of(const Args &a, int b) {
 __device__ __forceinline__ bool seq_is_bad(const Args &a, int b) {
     const int len = __ldg(a.seq_lens + b), q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
     return len < 0 || len > (a.max_pages << a.page_shift) || q0 < 0 || q1 < q0 || q1 > a.T ||
-           q1 - q0 > a.max_q;
+           q1 > q0 + a.max_q;
 }
 
 __device__ __forceinline__ int seq_tiles(const Seq &s) {
@@ -276,7 +275,7 @@ struct Chunks {
                 tiles = seq_tiles(seq);
             }
             const int cost = static_cast<int>(head_cost(a, tiles));
-            const uint32_t off = static_cast<uint32_t>(w - base);  // the host bounds cost * kv_heads
+            const uint32_t off = static_cast<uint32_t>(w - base);  // < cost * kv_heads < 2^30
             hk = static_cast<int>(off / static_cast<uint32_t>(cost));
             const int rel = static_cast<int>(off - static_cast<uint32_t>(hk) * cost);
             const int64_t left = min(static_cast<int64_t>(cost - rel), w_end - w);
@@ -362,6 +361,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // run of sequences, then the lane whose run holds the first position finds it
         const int per = (a.B + 31) / 32, b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
         int64_t mine = 0;
+#pragma unroll 4
         for (int b = b0; b < b1; ++b) mine += head_cost(a, seq_tiles(seq_of(a, b)));
         mine *= a.kv_heads;
         int64_t incl = mine;
@@ -631,17 +631,17 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const uint32_t tm = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const int G = a.group;
 
-        // sequences without positions, and reports
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-            if (st == 0 && seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
+        // sequences without positions, and reports: a warp per sequence
+        for (int b = blockIdx.x + sw * gridDim.x; b < a.B; b += kFewSoftmaxWarps * gridDim.x) {
+            if (lane == 0 && seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
             const Seq s = seq_of(a, b);
             if (s.len > 0) continue;
             for (int i = 0; i < s.q_len; ++i) {
                 const int64_t row = s.q0 + i;
                 uint4 *o = reinterpret_cast<uint4 *>(a.out + row * a.out_stride);
-                for (int c = st; c < a.q_heads * (kDim / 8); c += kThreads) o[c] = make_uint4(0, 0, 0, 0);
+                for (int c = lane; c < a.q_heads * (kDim / 8); c += 32) o[c] = make_uint4(0, 0, 0, 0);
                 if (a.lse != nullptr)
-                    for (int h = st; h < a.q_heads; h += kThreads) a.lse[row * a.q_heads + h] = -INFINITY;
+                    for (int h = lane; h < a.q_heads; h += 32) a.lse[row * a.q_heads + h] = -INFINITY;
             }
         }
 

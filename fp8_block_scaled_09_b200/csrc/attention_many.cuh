@@ -219,7 +219,7 @@ struct Items {
                 }
                 cost = tiles_until(a, seq, m * 256 + 256) + kItemCost;
             }
-            const uint32_t off = static_cast<uint32_t>(w - base);  // the host bounds cost * kv_heads
+            const uint32_t off = static_cast<uint32_t>(w - base);  // < cost * kv_heads < 2^30
             hk = static_cast<int>(off / static_cast<uint32_t>(cost));
             const int rel = static_cast<int>(off - static_cast<uint32_t>(hk) * cost);
             const int64_t left = min(static_cast<int64_t>(cost - rel), w_end - w);
@@ -695,9 +695,8 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int64_t q_row = sg->q0 + tok;
             float m_run = -INFINITY, l_run = 0.0f;
             if (n > 0) {
-                // the row's query: power of two that takes its largest channel to
-                // [128, 256), two E4M3 parts, K-major with the 128-byte swizzle
-                // The warp fetches two rows at a time (a thread its own row would touch 32
+                // The row's query: power of two that takes its largest channel to
+                // [128, 256), two E4M3 parts, K-major with the 128-byte swizzle.  The warp fetches two rows at a time (a thread its own row would touch 32
                 // lines with each load) and hands them out through the rows' own places
                 // in shared memory.
                 // (This runs once per segment, from instructions that are no longer in the

@@ -703,10 +703,10 @@ cudaError_t launch_rms_norm(const DeviceInfo &d, const void *x, const void *resi
     return launch_rms_norm_v<4, 1024, 1>(x, residual, weight, eps, M, K, residual_out, q, s, h, st);
 }
 
-// Cache positions of one sequence: 32-bit in the kernels, with room for a tile.
-constexpr int64_t kMaxContext = int64_t(1) << 30;
-// Over all kv heads: 2^31 tiles of 128 with room for what heads and items add.
-constexpr int64_t kMaxHeadContext = int64_t(1) << 37;
+// Cache positions of one sequence: 2^18 tiles, which one CTA passes in about
+// half the time that a wait is given (the many-row kernel's work list waits
+// for whole segments).
+constexpr int64_t kMaxContext = int64_t(1) << 25;
 constexpr int64_t kMaxBatch = 65536;
 
 fp8bq_status check_attention(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads,
@@ -1042,7 +1042,7 @@ fp8bq_status fp8bq_paged_attention(const void *q_bf16, int64_t q_stride, const u
     while (shift < 20 && (int64_t(1) << shift) < page_size) ++shift;
     if (page_size < 8 || (int64_t(1) << shift) != page_size) return FP8BQ_ERR_UNSUPPORTED_SHAPE;
     if (q_stride % 8 != 0 || out_stride % 8 != 0 || slot_stride % 16 != 0 || num_slots > kMaxDim ||
-        max_pages > kMaxContext / page_size || max_pages * page_size > kMaxHeadContext / kv_heads || table_stride > kMaxBytes / 4 / std::max<int64_t>(B, 1))
+        max_pages > kMaxContext / page_size || table_stride > kMaxBytes / 4 / std::max<int64_t>(B, 1))
         return FP8BQ_ERR_UNSUPPORTED_SHAPE;
     if (T > 0 && (q_stride > kMaxBytes / 2 / T || out_stride > kMaxBytes / 2 / T))
         return FP8BQ_ERR_UNSUPPORTED_SHAPE;

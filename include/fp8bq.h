@@ -240,6 +240,7 @@ FP8BQ_API fp8bq_status fp8bq_gemm_silu_mul_quantize(const uint8_t *qa, const flo
  *                       is; may be the same buffer as residual_bf16 or x_bf16
  *   q_e4m3, s         : out, codes [M, K] and scales [M, K/128]; both or neither
  *   h_bf16            : out, optional BF16 [M, K], BF16(h); required without q_e4m3
+ * The sum of squares is FP32: |r| below 2^60.
  * K a multiple of 128, at most 32768; eps >= 0 and finite.  Other than the
  * aliasing named above, buffers must not overlap.
  */
@@ -329,8 +330,7 @@ FP8BQ_API fp8bq_status fp8bq_rope_kv_write_e4m3(
  *                      kv_heads, max_q_len) bytes, same state rule as fp8bq_gemm
  *                      (one workspace may serve both, in stream order)
  * Heads have 128 channels; q_heads a multiple of kv_heads, at most 1024;
- * page_size a power of two from 8 to 2^20, max_pages * page_size <= 2^30 (2^37 over
- * all kv heads);
+ * page_size a power of two from 8 to 2^20, max_pages * page_size <= 2^25;
  * B <= 65536, T < 2^21; scale > 0; q, out and the caches 16-byte aligned,
  * q_stride and out_stride multiples of 8, slot_stride of 16.
  * Slots at or behind a sequence's length may hold anything, NaN codes too;

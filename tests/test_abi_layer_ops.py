@@ -72,7 +72,7 @@ def test_attention_argument_errors(L):
         assert f(scale=s) == INVALID
     for p in (0, 1, 4, 12, 24, 48, 1 << 21, -16):
         assert f(page=p) == SHAPE, p
-    assert f(mp=1 << 27, ts=1 << 27) == SHAPE                        # beyond 2^30 positions
+    assert f(mp=(1 << 21) + 1, ts=1 << 22) == SHAPE                  # beyond 2^25 positions
     assert f(qs=504) == INVALID and f(os=504) == INVALID and f(ss=240) == INVALID
     assert f(qs=516) == SHAPE and f(os=516) == SHAPE and f(ss=264) == SHAPE
     assert f(slots=1 << 31) == SHAPE

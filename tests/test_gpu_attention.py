@@ -54,7 +54,9 @@ def check(c, out, lse, q_heads, kv_heads, page, causal=True, scale=None):
 HEADS = [(56, 8), (28, 4), (8, 8), (7, 1), (12, 4), (16, 2)]
 DECODE_CTX = [[1], [127, 128, 129], [0, 1, 700, 0, 64, 2049], [3000] * 5, [15, 16, 17, 33, 1], [6150],
               # several sequences and chunks for each CTA
-              [37 * i % 2900 for i in range(90)]]
+              [37 * i % 2900 for i in range(90)],
+              # more sequences than CTAs, most of them shorter than a tile, some empty
+              [i * 7 % 41 for i in range(700)]]
 
 
 @pytest.mark.parametrize("page", [8, 16, 64, 128, 512])
@@ -174,6 +176,58 @@ def test_device_side_checks(n):
                           16, 7, 1, n + 1, out=out.t)
     assert fp8bq.last_device_status() == 8 and out.guards_intact()
     assert torch.equal(out.t[:2 * n].cpu(), good[:2 * n])
+
+
+@pytest.mark.parametrize("n", [1, 30])
+def test_cache_beyond_4_gib(n):
+    """Pages whose bytes lie behind 2^32, written by the rotary call and read by attention."""
+    heads, kv, page, ctx = 14, 2, 64, 200
+    slots = (1 << 32) // 256 + 64 * page
+    kc, vc = (torch.empty(slots, kv * 128, dtype=torch.uint8, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(n)
+    table = (slots // page - 1 - torch.randperm(8, generator=g)[:4]).int().view(1, 4)
+    pos = torch.arange(ctx)
+    loc = table[0].long()[pos // page] * page + pos % page
+    assert int(loc.min()) * kv * 128 > 1 << 32
+    qkv = torch.randn(ctx, (heads + 2 * kv) * 128, generator=g).bfloat16()
+    freq = fp8bq.rope_inv_freq(128, 1e4, device="cuda")[0]
+    q = fp8bq.rope_kv_write_e4m3(qkv.cuda(), pos.cuda(), freq, loc.cuda(), kc, vc)[-n:]
+    out = fp8bq.paged_attention(q, kc, vc, table.cuda(), torch.tensor([ctx], dtype=torch.int32, device="cuda"),
+                                torch.tensor([0, n], dtype=torch.int32, device="cuda"), page, heads, kv, n)
+    # the same pages as a small cache
+    first = slots - 8 * page
+    y, size = ref.rope(qkv.view(ctx, -1, 128)[:, :heads + kv], pos, freq, 1.0, False)
+    k = ref.e4m3_values(kc[loc.cuda()]).view(ctx, kv, 128)
+    assert bool(((k - y[:, heads:]).abs() <= torch.maximum(ref.HALF_E4M3 * y[:, heads:].abs(), torch.tensor(ref.E4M3_SUB))
+                 + 2.0 ** -20 * size[:, heads:]).all())
+    o, _, bound, _ = ref.attention(q, kc[first:], vc[first:], table - first // page, torch.tensor([ctx]), torch.tensor([0, n]),
+                                   page, heads, kv, 128 ** -0.5, True)
+    assert bool(((out.cpu().double().view(o.shape) - o).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("n,heads", [(3, (7, 1)), (60, (7, 1)), (200, (2, 1))])
+def test_more_tokens_than_promised(n, heads):
+    """Tokens beyond max_q_len are skipped (their rows stay) and reported; those before them stand at
+    their positions among all of them.  Offsets that run backwards touch no other row."""
+    c = ref.random_batch([n, n], [n + 50, 300], *heads, 16, 8)
+    take = 2 if n == 3 else n - 7
+    o, _, bound, _ = ref.attention(c["q"], c["k_cache"], c["v_cache"], c["page_table"], c["seq_lens"], c["cu_q"], 16, *heads, 128 ** -0.5, True)
+    d = {k: v.cuda() for k, v in c.items()}
+    call = lambda cu, out, m: fp8bq.paged_attention(d["q"], d["k_cache"], d["v_cache"], d["page_table"], d["seq_lens"], cu,
+                                                    16, *heads, m, out=out)
+    out = torch.full_like(d["q"], 7.0)
+    call(d["cu_q"], out, take)
+    assert fp8bq.last_device_status() == 8
+    got = out.cpu().double().view(o.shape)
+    for b in range(2):
+        rows = slice(b * n, b * n + take)
+        assert bool(((got[rows] - o[rows]).abs() <= bound[rows]).all())
+        assert bool((got[b * n + take:(b + 1) * n] == 7).all())
+    for cu in ([0, n, 0], [n, 0, n], [-5, 0, -2 ** 31], [2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]):
+        out = Guarded(tuple(c["q"].shape), torch.bfloat16)
+        call(torch.tensor(cu, dtype=torch.int32, device="cuda"), out.t, n)
+        torch.cuda.synchronize()
+        assert out.guards_intact() and fp8bq.last_device_status() == 8
 
 
 def test_empty_batch_and_cache():
