@@ -34,6 +34,11 @@
 // thread: 128 scores), 2 converts V, warp 12 TMA producer, warp 13 MMA issuer,
 // warp 14 walks the work list and publishes the segments to the others (which
 // have no registers to spare for it: walking it in every role spilled scores).
+//
+// Measured: 2048 tokens of 56 + 8 heads at 18001 positions 811 us, 1.23 PFLOP/s (a pair
+// of halves takes ~3400 cycles per tile where its MMAs take 2048: the softmax chain
+// between them); a prompt of 8192 tokens 885 us; 16 blocks of 8 tokens of 28 + 4
+// heads at 1000 .. 8000 positions 45 us.
 #pragma once
 
 #include "attention_few.cuh"
@@ -47,7 +52,8 @@ constexpr int kSoftmaxRegs = 184, kConvertRegs = 56, kIssueRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <=
                   kManyThreads * kManyLaunchRegs,
               "register split exceeds the launch allocation");
-constexpr int kItemCost = 5;      // tiles' worth of work that an item adds
+// Tiles' worth of work that an item adds: 8192-token prompt 942 us; 1044 with 3, 952 with 6.
+constexpr int kItemCost = 5;
 constexpr int kManyMaxGrid = 160;
 constexpr int kHalfRows = 128;
 constexpr float kRescaleAt = 8.0f;  // log2

