@@ -38,6 +38,12 @@
 // position of the tile, its TMEM lane, in the score phase, one output channel
 // of half the rows in the merge), warp 10 queries, warp 11 follows the ring and clears
 // V behind a sequence's end.
+//
+// Measured, after a 256 MB write: 128 sequences of 2048 positions, 56 query and 8 kv
+// heads, pages of 64: 119 us, 4.5 TB/s; pages of 16: 141 us (a TMA box then brings only
+// 2 KB, and an SM starts one in ~80 ns; half of the pages by cp.async instead, from two
+// more warps, took 211 us).  One sequence of 65001 positions, among others of its kind:
+// 32 us, of which 5 pass before its first tile and 4 in the join.
 #pragma once
 
 #include "attention.cuh"

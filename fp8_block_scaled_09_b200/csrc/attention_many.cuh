@@ -33,7 +33,8 @@
 // Roles (512 threads): warpgroups 0 and 1 softmax of A and B (184 registers a
 // thread: 128 scores), 2 converts V, warp 12 TMA producer, warp 13 MMA issuer,
 // warp 14 walks the work list and publishes the segments to the others (which
-// have no registers to spare for it: walking it in every role spilled scores).
+// have no registers to spare for it: walking it in every role spilled scores), warp 15
+// writes the zeros of sequences without positions.
 //
 // Measured: 2048 tokens of 56 + 8 heads at 18001 positions 811 us, 1.23 PFLOP/s (a pair
 // of halves takes ~3400 cycles per tile where its MMAs take 2048: the softmax chain
@@ -171,9 +172,9 @@ __device__ __forceinline__ int row_limit(const Args &a, const Seq &s, int r) {
     return a.causal ? min(s.len - s.q_real + r / a.group, s.len - 1) : s.len - 1;
 }
 
-// 256-row blocks of a sequence.
+// 256-row blocks of a sequence; one without positions has no work, only zeros to write.
 __device__ __forceinline__ int row_blocks(const Args &a, const Seq &s) {
-    return (s.q_len * a.group + 255) / 256;
+    return s.len > 0 ? (s.q_len * a.group + 255) / 256 : 0;
 }
 
 // K/V tiles that rows [.., end) of a sequence need: at least one, which then
@@ -429,6 +430,31 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const uint32_t from = issued > F::kStages ? issued - F::kStages : 0;
             for (uint32_t i = from; i < issued; ++i)
                 mbar_wait(&full[i % F::kStages], (i / F::kStages) & 1, nullptr, status);
+        } else if (warp == 15) {
+            // -------------------------------------------------------- reports, empty sequences
+            // each CTA's share of the rows of sequences without positions, by row number
+            // (as items of the list with one masked tile they took 8 us each)
+            const int ctas = gridDim.x, cta = blockIdx.x;
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+                const int b = b0 + lane;
+                Seq s = {1, 0, 0, 0};
+                if (b < a.B) {
+                    s = seq_of(a, b);
+                    if (cta == 0 && seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
+                }
+                unsigned todo = __ballot_sync(0xFFFFFFFFu, s.len == 0 && s.q_len > 0);
+                for (; todo != 0; todo &= todo - 1) {
+                    const int l = __ffs(todo) - 1;
+                    const int q0 = __shfl_sync(0xFFFFFFFFu, s.q0, l), n = __shfl_sync(0xFFFFFFFFu, s.q_len, l);
+                    for (int i = (cta + ctas - q0 % ctas) % ctas; i < n; i += ctas) {
+                        const int64_t row = q0 + i;
+                        uint4 *o = reinterpret_cast<uint4 *>(a.out + row * a.out_stride);
+                        for (int c = lane; c < a.q_heads * (kDim / 8); c += 32) o[c] = make_uint4(0, 0, 0, 0);
+                        if (a.lse != nullptr)
+                            for (int h = lane; h < a.q_heads; h += 32) a.lse[row * a.q_heads + h] = -INFINITY;
+                    }
+                }
+            }
         } else if (warp == 14) {
             // -------------------------------------------------------- work list
             if (lane == 0) {
@@ -671,9 +697,6 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_tm = tmem + lanes + F::s_col(half), o_tm = tmem + lanes + F::o_col(half);
         const int G = a.group;
-
-        for (int b = blockIdx.x * 256 + threadIdx.x; b < a.B; b += gridDim.x * 256)
-            if (seq_is_bad(a, b)) atomicExch(status, 8 /* FP8BQ_ERR_INDEX */);
 
         // 16 bytes number c of a 256-byte row of this warp, in the places of the row's query parts
         auto staged = [&](int row, int c) {
