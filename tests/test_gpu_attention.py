@@ -90,7 +90,10 @@ def test_few_tokens(q_lens, ctx, heads, page, causal):
     # blocks of up to 64, 128 and 256 rows, whole and split, several for each CTA
     ([5 + i % 15 for i in range(40)], [29 * i % 1200 for i in range(40)], (56, 8), 16),
     ([40 + i % 60 for i in range(24)], [37 * i % 1000 for i in range(24)], (28, 4), 64),
-    ([5] * 3, [9000, 3, 4000], (56, 8), 64), ([600] * 2, [600, 0], (8, 8), 128)])
+    ([5] * 3, [9000, 3, 4000], (56, 8), 64), ([600] * 2, [600, 0], (8, 8), 128),
+    # sequences without positions: first and last, between others, all of them, more than 32
+    ([700, 5, 0, 64, 300, 41], [0, 5, 0, 0, 700, 0], (28, 4), 16), ([300, 40], [0, 0], (7, 1), 64),
+    ([17 + i % 5 for i in range(90)], [(i % 3) * 31 * i % 500 for i in range(90)], (8, 8), 32)])
 def test_chunks(q_lens, ctx, heads, page, causal):
     c = ref.random_batch(q_lens, ctx, *heads, page, 70 + len(ctx))
     check(c, *run(c, *heads, page, causal, pad_rows=1), *heads, page, causal)

@@ -59,7 +59,11 @@ def _check_codes(q, s, h):
     (1, 128, True, "normal"), (1, 7168, True, "normal"), (3, 7168, False, "normal"),
     (17, 8320, True, "normal"), (5, 16512, True, "normal"), (2, 32768, True, "normal"),
     (700, 1024, True, "normal"), (5000, 256, False, "normal"), (6, 1152, True, "zero"),
-    (6, 1152, False, "large"), (6, 1152, True, "tiny"), (333, 7168, True, "normal")])
+    (6, 1152, False, "large"), (6, 1152, True, "tiny"), (333, 7168, True, "normal"),
+    # both sides of the sizes at which rows are held by other numbers of threads
+    (148, 8192, True, "normal"), (149, 8192, False, "normal"), (592, 2048, True, "normal"),
+    (593, 2048, True, "normal"), (296, 4096, False, "normal"), (149, 4224, True, "normal"),
+    (148, 8320, False, "normal"), (149, 8320, True, "normal"), (40, 16384, True, "normal")])
 def test_norm_quantize(M, K, residual, kind):
     x, r, w = _norm_inputs(M, K, M + K, kind)
     xd, rd, wd = x.cuda(), r.cuda(), w.cuda()
