@@ -90,6 +90,20 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_mn(int m, int n) {
     return umma_idesc_e4m3(m, n) | (1u << 15) | (1u << 16);
 }
 
+// True in one lane of the (converged) warp.  MMA issuers that let the whole warp
+// run their loops and only issue in this lane keep descriptors and addresses in
+// uniform registers, where the MMA instruction wants them; in a branch on the lane
+// number each is moved there before every MMA (~100 cycles per MMA measured).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Unswizzled operand tile whose M or N dimension is contiguous: blocks of 16
 // bytes of it by 8 K rows (128 bytes); `k_step` bytes between blocks along K,
 // `mn_step` along M or N.

@@ -105,6 +105,14 @@ __device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// 16-byte asynchronous global -> shared copy (completion: cp_async_wait_all); the
+// bytes from src_bytes (0 or 16) on are zeros.
+__device__ __forceinline__ void cp_async_16(void *smem_dst, const void *gmem_src, uint32_t src_bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem_dst)),
+                 "l"(gmem_src), "r"(src_bytes)
+                 : "memory");
+}
+
 // 32 consecutive columns of this warp's lanes, without the wait.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
     uint32_t *r = reinterpret_cast<uint32_t *>(v);

@@ -270,20 +270,6 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// True in one lane of the (converged) warp.  MMA issuers that let the whole warp
-// run their loops and only issue in this lane keep descriptors and addresses in
-// uniform registers, where the MMA instruction wants them; in a branch on the lane
-// number each is moved there before every MMA (~100 cycles per MMA measured).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
-
 // Arrive once on `bar` when all previously issued tcgen05 MMAs of this thread finish.
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
     asm volatile(
@@ -374,13 +360,6 @@ __device__ __forceinline__ void allow_dependent_launch() {
 __device__ __forceinline__ void cp_async_4(void *smem_dst, const void *gmem_src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(smem_dst)),
                  "l"(gmem_src)
-                 : "memory");
-}
-
-// 16-byte one; the bytes from src_bytes (0 or 16) on are zeros.
-__device__ __forceinline__ void cp_async_16(void *smem_dst, const void *gmem_src, uint32_t src_bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem_dst)),
-                 "l"(gmem_src), "r"(src_bytes)
                  : "memory");
 }
 
