@@ -733,9 +733,9 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             float m_run = -INFINITY, l_run = 0.0f;
             if (n > 0) {
                 // The row's query: power of two that takes its largest channel to
-                // [128, 256), two E4M3 parts, K-major with the 128-byte swizzle.  The warp fetches two rows at a time (a thread its own row would touch 32
-                // lines with each load) and hands them out through the rows' own places
-                // in shared memory.
+                // [128, 256), two E4M3 parts, K-major with the 128-byte swizzle.  The warp
+                // fetches two rows at a time (a thread its own row would touch 32 lines with
+                // each load) and hands them out through the rows' own places in shared memory.
                 // (This runs once per segment, from instructions that are no longer in the
                 // cache: short loops, since each new line of code costs more than its work.)
                 const int64_t at = live ? q_row * a.q_stride + static_cast<int64_t>(head) * kDim : -1;

@@ -20,7 +20,8 @@
 // one scale.  The weight stays in L1.  Measured: 8192 x 7168 to BF16 70.6 us,
 // 6.65 TB/s; 2048 x 7168 with residual and codes 21.6 us, 4.8 TB/s (the start and
 // the last wave of a short kernel), 8192 rows of it 76.3 us, 5.4 TB/s.  Packed
-// FP32 pairs for the products were no faster.
+// FP32 pairs for the products were no faster; CTAs that stay and fetch their next
+// row ahead were slower (23.7 and 85.5 us): their registers leave two rows per SM.
 #pragma once
 
 #include <cuda_bf16.h>
