@@ -11,13 +11,17 @@
 //     O^T[ch, row] += V[:, ch]^T . P[:, row]      M = 128, N = 2 NR, K = 128 positions
 // Neither K nor V is ever converted: V is the A operand with its channels
 // contiguous.  Queries and weights keep their precision as two E4M3 parts,
-// x = hi + lo, in two columns whose results are added: hi holds 4 significant
-// bits, lo the next 4, so a BF16 query is exact down to 2^-9 of its row's
-// largest channel (rows are scaled by a power of two to [128, 256)), and a
-// weight p (scaled by 256) has 8 bits down to 2^-10 of the largest and an
-// absolute error of 2^-18 below.  (Two MMAs into one column cost more: an MMA
-// with this few columns takes the time to read its 4 KB of A, and with twice
-// as many of them the tensor pipe was busy 1100 of 2550 cycles per tile.)
+// in two columns whose results are added: hi holds 4 significant bits, lo the
+// next 4.  A BF16 query x = hi + lo is exact down to 2^-9 of its row's
+// largest channel (rows are scaled by a power of two to [128, 256)).  A weight
+// p = hi + lo / 32, held times a power of two that takes the chunk's largest to
+// (128, 256], has 8 bits down to 2^-15 of that and an absolute error of 2^-23
+// of 256 below: hi's error is at most 8, so 32 times it stays below 256.  (Without
+// the 32 the steps were 2^-17 of the largest: a first position 13 logits above
+// 32768 others of its own value near 0 took 21% off the output.)  Two MMAs into one
+// column cost more: an MMA with this few columns takes the time to read its
+// 4 KB of A, and with twice as many of them the tensor pipe was busy 1100 of 2550
+// cycles per tile.
 //
 // Work is a list of tiles of 128 positions, ordered by (sequence, kv head,
 // tile), each head preceded by some tiles' worth of nothing for what
@@ -26,8 +30,13 @@
 // (sequence, head), its segment, are taken in chunks of at most kChunk tiles,
 // as many as TMEM holds scores for (twice): a chunk's scores are all there
 // before its softmax, so no output is ever rescaled in TMEM; the chunk's O^T is
-// merged into registers with the usual factor exp(m_old - m_new), one chunk
-// later, so that nothing waits for its MMAs.  The ring carries K of chunk
+// merged into registers with a factor 2^(r_old - r_new), one chunk
+// later, so that nothing waits for its MMAs.  r, the reference that a chunk's
+// weights are held against, is the chunk's own maximum rounded up to an integer
+// (in log2: factors are exact), not the running one: a position that dominates the
+// row then coarsens only the weights of its own chunk.  Where a chunk lies more than
+// kFarBelow under the running maximum, r stays there, so that no sum overflows; what
+// is lost then is 2^-86 of the row's largest weight.  The ring carries K of chunk
 // g + 1 ahead of V of chunk g, so the next scores are computed while the
 // softmax works.  A (sequence, head) that lies in several CTAs leaves FP32
 // partials and maxima in the workspace; the last CTA to arrive (a counter)
@@ -57,7 +66,10 @@ constexpr int kTile = 128;                 // positions
 constexpr int kStageBytes = kTile * kDim;  // one K or V tile of codes
 constexpr int kFewSoftmaxWarps = 8;
 constexpr int kFewThreads = 32 * (4 + kFewSoftmaxWarps);
-constexpr float kPScale = 8.0f;  // weights are held times 2^8
+constexpr float kPScale = 8.0f;    // weights are held times 2^8
+constexpr float kLoScale = 32.0f;  // their low parts times 2^5 more
+// log2: sums stay below 2^(8 + 25 + 64), outputs below 2^9 times that
+constexpr float kFarBelow = 64.0f;
 
 template <int NR>
 struct Few {
@@ -74,13 +86,13 @@ struct Few {
     static constexpr int kBarOff = kPOff + kPSlots * kP;
     // full, empty, cleared; pfull, pempty; qfull (4), qempty, sfull, sfree, ofull, ofree (2 each)
     static constexpr int kBars = 3 * kStages + 2 * kPSlots + 4 + 10;
-    // per-row values: scale and limit [4], maximum and factor [2], negated maximum,
-    // reductions over the warps [8], sums over the warps [2][8]
+    // per-row values: scale and limit [4], reference and factor [2], negated reference,
+    // running maximum, reductions over the warps [8], sums over the warps [2][8]
     static constexpr int kRowOff = kBarOff + kBars * 8;
-    static constexpr int kBytes = kRowOff + (4 + 4 + 2 + 2 + 1 + 8 + 16) * NR * 4 + 64 + 1024;
+    static constexpr int kBytes = kRowOff + (4 + 4 + 2 + 2 + 1 + 1 + 8 + 16) * NR * 4 + 64 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory");
     static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kQ % 1024 == 0, "swizzled tiles");
-    static constexpr int kPartial = NR * (kDim + 2);  // floats: O [NR][128], max [NR], sum [NR]
+    static constexpr int kPartial = NR * (kDim + 2);  // floats: O [NR][128], reference [NR], sum [NR]
     __device__ static uint32_t s_col(int buf, int j) { return (buf * kChunk + j) * kN; }
     __device__ static uint32_t o_col(int buf) { return (2 * kChunk + buf) * kN; }
 };
@@ -179,11 +191,12 @@ __device__ __forceinline__ void split8(uint4 v, float up, uint2 &hi, uint2 &lo) 
                     e4m3x2_satfinite(x[4], x[5]) | (static_cast<uint32_t>(e4m3x2_satfinite(x[6], x[7])) << 16));
 }
 
-// Two E4M3 codes -> two floats (exact).
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
+// Two E4M3 codes -> two floats, -kLoScale times their values (exact in F16: 4
+// significant bits, at most 2^14).
+__device__ __forceinline__ float2 e4m3x2_to_neg_scaled(uint16_t c) {
     uint32_t h2;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+    return __half22float2(__hmul2(*reinterpret_cast<const __half2 *>(&h2), __float2half2_rn(-kLoScale)));
 }
 
 // A sequence as the kernels take it: lengths that the host cannot check are
@@ -333,10 +346,11 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
              *sfree = sfull + 2, *ofull = sfree + 2, *ofree = ofull + 2, *cleared = ofree + 2;
     float *row_scale = reinterpret_cast<float *>(smem + F::kRowOff);  // [4] score -> log2 weight
     int *row_lim = reinterpret_cast<int *>(row_scale + 4 * NR);       // [4] last position seen
-    float *row_max = reinterpret_cast<float *>(row_lim + 4 * NR);     // [2] maximum (log2), by chunk
-    float *row_fac = row_max + 2 * NR;   // [2] exp2(old maximum - new), by chunk
-    float *row_neg = row_fac + 2 * NR;   // kPScale - maximum
-    float *row_red = row_neg + NR;       // [8] maxima per softmax warp
+    float *row_ref = reinterpret_cast<float *>(row_lim + 4 * NR);     // [2] reference (log2), by chunk
+    float *row_fac = row_ref + 2 * NR;   // [2] exp2(old reference - new), by chunk
+    float *row_neg = row_fac + 2 * NR;   // kPScale - reference
+    float *row_top = row_neg + NR;       // running maximum, rounded up
+    float *row_red = row_top + NR;       // [8] maxima per softmax warp
     float *row_sum = row_red + 8 * NR;   // [2][8] sums per softmax warp, by chunk
     uint32_t *misc = reinterpret_cast<uint32_t *>(row_sum + 16 * NR);
     uint32_t *tmem_slot = misc;
@@ -702,12 +716,12 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (lane == 0) mbar_arrive(&ofree[buf]);
 #pragma unroll
             for (int k = 0; k < kHalf; ++k) {
-                const float o = hi[k] + lo[k];
+                const float o = fmaf(lo[k], 1.0f / kLoScale, hi[k]);
                 o_run[k] = prev.first ? o : fmaf(o_run[k], row_fac[buf * NR + group * kHalf + k], o);
             }
             if (!prev.last) return;
             const int rows = prev.rows;
-            const float *m_row = row_max + buf * NR, *sums = row_sum + buf * 8 * NR;
+            const float *m_row = row_ref + buf * NR, *sums = row_sum + buf * 8 * NR;
             auto total = [&](int r) {
                 float l = 0.0f;
 #pragma unroll
@@ -847,10 +861,12 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 float m = row_red[st];
 #pragma unroll
                 for (int w = 1; w < kFewSoftmaxWarps; ++w) m = fmaxf(m, row_red[w * NR + st]);
-                m *= scale[st];  // -inf stays: nothing of the chunk is seen
-                const float old = cur.first ? -INFINITY : row_max[(buf ^ 1) * NR + st];
-                m = fmaxf(m, old);
-                row_max[buf * NR + st] = m;
+                m = ceilf(m * scale[st]);  // -inf stays: nothing of the chunk is seen
+                const float old = cur.first ? -INFINITY : row_ref[(buf ^ 1) * NR + st];
+                const float top = cur.first ? m : fmaxf(m, row_top[st]);
+                m = fmaxf(m, top - kFarBelow);
+                row_top[st] = top;
+                row_ref[buf * NR + st] = m;
                 row_neg[st] = m == -INFINITY ? 0.0f : kPScale - m;
                 row_fac[buf * NR + st] = m == -INFINITY ? 1.0f : ex2(old - m);
             }
@@ -875,10 +891,12 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 for (int r = 0; r < NR; r += 4) {
                     const uint16_t h0 = e4m3x2_satfinite(v[r], v[r + 1]);
                     const uint16_t h1 = e4m3x2_satfinite(v[r + 2], v[r + 3]);
-                    const float2 d0 = e4m3x2_to_float2(h0), d1 = e4m3x2_to_float2(h1);
+                    const float2 d0 = e4m3x2_to_neg_scaled(h0), d1 = e4m3x2_to_neg_scaled(h1);
                     hi[r / 4] = h0 | (static_cast<uint32_t>(h1) << 16);
-                    lo[r / 4] = e4m3x2_satfinite(v[r] - d0.x, v[r + 1] - d0.y) |
-                                (static_cast<uint32_t>(e4m3x2_satfinite(v[r + 2] - d1.x, v[r + 3] - d1.y)) << 16);
+                    lo[r / 4] = e4m3x2_satfinite(fmaf(v[r], kLoScale, d0.x), fmaf(v[r + 1], kLoScale, d0.y)) |
+                                (static_cast<uint32_t>(e4m3x2_satfinite(fmaf(v[r + 2], kLoScale, d1.x),
+                                                                        fmaf(v[r + 3], kLoScale, d1.y)))
+                                 << 16);
                 }
 #pragma unroll
                 for (int r = 0; r < NR; ++r) l_run[r] += v[r];
