@@ -17,8 +17,10 @@
 // exponentials (16 a cycle and SM: 1024 cycles per half and tile): the halves
 // alternate, one's softmax under the other's MMAs.  A softmax thread has a whole
 // row, so maxima and sums need no exchange.  The running maximum is only
-// moved when a row's scores pass it by 2^8 (weights up to 2^8 are as exact in
-// F16 and FP32), so O is hardly ever rescaled in the tensor memory.
+// moved when a row's scores pass it by 2^8, so O is hardly ever rescaled in the
+// tensor memory; weights are held times 2^7, so that they reach 2^15 at most and
+// those far below a dominant position keep a step of 2^-31 of it or less (without the
+// 2^7, what 32768 positions 18 logits under the first one add up to was lost).
 //
 // Blocks of at most 128 rows have no second half: there both halves hold the same
 // rows and take the tiles in turn; B hands its result to A through the shared
@@ -58,6 +60,7 @@ constexpr int kItemCost = 5;
 constexpr int kManyMaxGrid = 160;
 constexpr int kHalfRows = 128;
 constexpr float kRescaleAt = 8.0f;  // log2
+constexpr float kWeightLog2 = 7.0f;  // weights are held times 2^7: with kRescaleAt at most 2^15
 
 struct Many {
     static constexpr int kStages = 6;  // K tiles in even, V tiles in odd stages
@@ -831,7 +834,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             }
                         }
                     }
-                    const float neg = m_run == -INFINITY ? 0.0f : -m_run;
+                    const float neg = m_run == -INFINITY ? 0.0f : kWeightLog2 - m_run;
                     const float2 s2 = make_float2(scale, scale), n2 = make_float2(neg, neg);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -945,7 +948,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             auto store_lse = [&](float m, float l) {
                 if (live && a.lse != nullptr)
                     a.lse[q_row * a.q_heads + head] =
-                        l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        l > 0.0f ? (m - kWeightLog2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
             };
             if (sg->whole) {
                 const float f = l_run > 0.0f ? __fdividef(256.0f, l_run) : 0.0f;

@@ -336,7 +336,8 @@ FP8BQ_API fp8bq_status fp8bq_rope_kv_write_e4m3(
  * Scores, softmax sums and outputs are accumulated in FP32.  The weights that
  * multiply V are rounded, those of the sums are not: up to 16 new tokens x heads of
  * a group to 2^-8 of themselves, or 2^-22 of the largest weight within the
- * same run of at most 1920 positions if that is more; above, to 11 bits (F16).
+ * same run of at most 1920 positions if that is more; above, to 2^-11 of themselves,
+ * or 2^-32 of the row's largest.
  * Slots at or behind a sequence's length may hold anything, NaN codes too;
  * the cache positions that a sequence has must hold finite values, and q too.
  * Rows of q and out at or behind cu_q[B] are padding: neither read nor written.

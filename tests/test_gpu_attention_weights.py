@@ -135,3 +135,32 @@ def test_few_and_many_rows_agree(positions, gap):
     check(one, few, few_lse, group, 1, range(batch))
     # each within the weights' 2^-8, rounded to BF16
     assert bool(((few - many[last]).abs() <= 2.0 ** -6 * many[last].abs() + 1920 * 2.0 ** -22).all())
+
+
+@pytest.mark.parametrize("tokens", [3, 37])
+@pytest.mark.parametrize("gap", [14.0, 18.0, 20.0])
+def test_many_rows_under_a_dominant_position_without_a_value(gap, tokens):
+    """Here the output is what the far positions leave: weights of 2^-20 to 2^-29 of the largest.  The weights
+    of the many-row kernel are F16, 2^7 and more at the largest, so within 2^-11 of themselves or 2^-32 of the
+    largest (half of F16's smallest step, 2^-25, over 2^7)."""
+    group, n, page, batch = 7, 32768, 64, whole_heads()
+    c = dominated(n, gap, 0, group, tokens, batch, page, int(gap))
+    first = int(c["page_table"][0, 0]) * page
+    c["v_cache"][first] = 0
+    out, lse = attend(c, group, tokens, page)
+    slot = (c["page_table"][0].long()[:, None] * page + torch.arange(page)).reshape(-1)
+    k, v = (ref.e4m3_values(x)[slot] for x in (c["k_cache"], c["v_cache"]))
+    for row in (0, tokens - 1, (batch // 2) * tokens, batch * tokens - 1):
+        x = c["q"][row].double().view(group, 128)
+        seen = n - tokens + row % tokens + 1
+        z = x @ k[:seen].T * SCALE
+        l = z.logsumexp(1)
+        w = (z - l[:, None]).exp()
+        o = w @ v[:seen]
+        dz = SCALE * (2.0 ** -17 * x.abs().amax(1) * k.abs().sum(1).max() +
+                      128 * 2.0 ** -23 * (x.abs() @ k[:seen].abs().T).amax(1))
+        bound = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2 * dz[:, None]) * (w @ v[:seen].abs()) + \
+            2.0 ** -32 * w.amax(1, keepdim=True) * v[:seen].abs().sum(0)
+        err = (out[row] - o).abs()
+        assert bool((err <= bound).all()), (row, float((err / bound).max()), float((err / o.abs()).max()))
+        assert bool(((lse[row] - l).abs() <= dz + 2.0 ** -15).all())
