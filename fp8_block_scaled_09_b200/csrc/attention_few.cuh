@@ -12,11 +12,12 @@
 // Neither K nor V is ever converted: V is the A operand with its channels
 // contiguous.  Queries and weights keep their precision as two E4M3 parts,
 // in two columns whose results are added: hi holds 4 significant bits, lo the
-// next 4.  A BF16 query x = hi + lo is exact down to 2^-9 of its row's
-// largest channel (rows are scaled by a power of two to [128, 256)).  A weight
-// p = hi + lo / 32, held times a power of two that takes the chunk's largest to
-// (128, 256], has 8 bits down to 2^-15 of that and an absolute error of 2^-23
-// of 256 below: hi's error is at most 8, so 32 times it stays below 256.  (Without
+// next 4, x = hi + lo / 32: of x up to 256 hi's error is at most 8, so 32 times
+// it stays below 256.  A BF16 query, scaled by a power of two that takes its row's
+// largest channel to [128, 256), is exact down to 2^-14 of that and off by at most
+// 2^-22 of it below.  A weight, held times a power of two that takes the chunk's
+// largest to (128, 256], has 8 bits down to 2^-15 of that and an absolute error of 2^-23
+// of 256 below.  (Without
 // the 32 the steps were 2^-17 of the largest: a first position 13 logits above
 // 32768 others of its own value near 0 took 21% off the output.)  Two MMAs into one
 // column cost more: an MMA with this few columns takes the time to read its
@@ -67,7 +68,7 @@ constexpr int kStageBytes = kTile * kDim;  // one K or V tile of codes
 constexpr int kFewSoftmaxWarps = 8;
 constexpr int kFewThreads = 32 * (4 + kFewSoftmaxWarps);
 constexpr float kPScale = 8.0f;    // weights are held times 2^8
-constexpr float kLoScale = 32.0f;  // their low parts times 2^5 more
+constexpr float kLoScale = 32.0f;  // low parts, of queries too, times 2^5 more
 // log2: sums stay below 2^(8 + 25 + 64), outputs below 2^9 times that
 constexpr float kFarBelow = 64.0f;
 
@@ -197,6 +198,22 @@ __device__ __forceinline__ float2 e4m3x2_to_neg_scaled(uint16_t c) {
     uint32_t h2;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
     return __half22float2(__hmul2(*reinterpret_cast<const __half2 *>(&h2), __float2half2_rn(-kLoScale)));
+}
+
+// Eight BF16 values times `up` (as in split8) as two E4M3 parts for columns of their own.
+__device__ __forceinline__ void split8_scaled(uint4 v, float up, uint2 &hi, uint2 &lo) {
+    float x[8];
+    unpack_bf16x8(v, x);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float a = x[2 * k] * up, b = x[2 * k + 1] * up;
+        h[k] = e4m3x2_satfinite(a, b);
+        const float2 d = e4m3x2_to_neg_scaled(static_cast<uint16_t>(h[k]));
+        l[k] = e4m3x2_satfinite(fmaf(a, kLoScale, d.x), fmaf(b, kLoScale, d.y));
+    }
+    hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
 }
 
 // A sequence as the kernels take it: lengths that the host cannot check are
@@ -600,7 +617,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int e = max(static_cast<int>(m >> 7) - 127, -100);
                 const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
                 uint2 hi, lo;
-                split8(u, up, hi, lo);
+                split8_scaled(u, up, hi, lo);
                 // rows r and NR + r have the same place in their 8-row swizzle group
                 const int off = r * kDim + (((sub >> 1) ^ (r & 7)) << 4) + (sub & 1) * 8;
                 *reinterpret_cast<uint2 *>(dst + off) = hi;
@@ -823,7 +840,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_wait(&sfull[buf], (g >> 1) & 1, abort_flag, status);
             tc_fence_after_sync();
 
-            // scores of tile j: hi + lo
+            // scores of tile j: hi + lo / 32
             auto load_scores = [&](int j, auto &v) {
                 float lo[NR];
                 tmem_ld<NR>(tm + F::s_col(buf, j), v);
@@ -831,7 +848,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 tmem_ld_wait<NR>(v);
                 tmem_ld_wait<NR>(lo);
 #pragma unroll
-                for (int r = 0; r < NR; ++r) v[r] += lo[r];
+                for (int r = 0; r < NR; ++r) v[r] = fmaf(lo[r], 1.0f / kLoScale, v[r]);
             };
 
             // pass 1: the chunk's maximum of every row

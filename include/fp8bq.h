@@ -333,11 +333,12 @@ FP8BQ_API fp8bq_status fp8bq_rope_kv_write_e4m3(
  * page_size a power of two from 8 to 2^20, max_pages * page_size <= 2^25;
  * B <= 65536, T < 2^21; scale > 0; q, out and the caches 16-byte aligned,
  * q_stride and out_stride multiples of 8, slot_stride of 16.
- * Scores, softmax sums and outputs are accumulated in FP32.  The weights that
- * multiply V are rounded, those of the sums are not: up to 16 new tokens x heads of
- * a group to 2^-8 of themselves, or 2^-22 of the largest weight within the
- * same run of at most 1920 positions if that is more; above, to 2^-11 of themselves,
- * or 2^-32 of the row's largest.
+ * Scores, softmax sums and outputs are accumulated in FP32.  What multiplies K
+ * and V is rounded, the sums' weights are not.  Up to 16 new tokens x heads of a
+ * group: queries exact down to 2^-14 of a row's largest channel and within 2^-22 of
+ * it below; weights within 2^-8 of themselves, or 2^-22 of the largest weight in
+ * the same run of at most 1920 positions if that is more.  Above 16: queries exact
+ * down to 2^-9 and within 2^-17; weights within 2^-11, or 2^-32 of the row's largest.
  * Slots at or behind a sequence's length may hold anything, NaN codes too;
  * the cache positions that a sequence has must hold finite values, and q too.
  * Rows of q and out at or behind cu_q[B] are padding: neither read nor written.

@@ -164,3 +164,36 @@ def test_many_rows_under_a_dominant_position_without_a_value(gap, tokens):
         err = (out[row] - o).abs()
         assert bool((err <= bound).all()), (row, float((err / bound).max()), float((err / o.abs()).max()))
         assert bool(((lse[row] - l).abs() <= dz + 2.0 ** -15).all())
+
+
+@pytest.mark.parametrize("group,tokens", [(7, 1), (16, 1), (8, 2)])
+@pytest.mark.parametrize("loud", [1.0, 60.0, 4096.0, 16384.0])
+def test_a_loud_query_channel(loud, group, tokens):
+    """One channel of every query far above the others, where the keys have nothing: the scores come from the
+    quiet ones.  Few-row queries are within 2^-22 of their largest channel (BF16 exact from 2^-14 of it on)."""
+    n, page, batch = 700, 16, 3
+    g = torch.Generator().manual_seed(int(loud) + group)
+    pages = -(-n // page)
+    k, v = torch.randn(pages * page, 128, generator=g), torch.randn(pages * page, 128, generator=g)
+    k[:, 77] = 0
+    q = 1.5 * torch.randn(batch * tokens, group, 128, generator=g)
+    q[..., 77] = loud
+    c = {"q": q.bfloat16().view(batch * tokens, -1), "k_cache": k.to(torch.float8_e4m3fn).view(torch.uint8),
+         "v_cache": v.to(torch.float8_e4m3fn).view(torch.uint8), "page_table": torch.arange(pages).int().expand(batch, -1).contiguous(),
+         "seq_lens": torch.full((batch,), n, dtype=torch.int32), "cu_q": torch.arange(batch + 1, dtype=torch.int32) * tokens}
+    out, lse = attend(c, group, tokens, page)
+    kd, vd = (ref.e4m3_values(c[x])[:n] for x in ("k_cache", "v_cache"))
+    for row in range(batch * tokens):
+        seen = n - tokens + row % tokens + 1
+        x = c["q"][row].double().view(group, 128)
+        z = x @ kd[:seen].T * SCALE
+        l = z.logsumexp(1)
+        w = (z - l[:, None]).exp()
+        o = w @ vd[:seen]
+        top = x.abs().amax(1, keepdim=True)
+        off = (x.abs() < 2.0 ** -14 * top) * 2.0 ** -22 * top
+        dz = SCALE * ((off @ kd[:seen].abs().T).amax(1) + 128 * 2.0 ** -23 * (x.abs() @ kd[:seen].abs().T).amax(1))
+        bound = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2 * dz[:, None]) * (w @ vd[:seen].abs()) + \
+            n * 2.0 ** -22 * w.amax(1, keepdim=True) * vd.abs().max()
+        assert bool(((out[row] - o).abs() <= bound).all()), float(((out[row] - o).abs() / bound).max())
+        assert bool(((lse[row] - l).abs() <= dz + 2.0 ** -15).all()), float((lse[row] - l).abs().max())
