@@ -69,6 +69,9 @@ constexpr int kFewSoftmaxWarps = 8;
 constexpr int kFewThreads = 32 * (4 + kFewSoftmaxWarps);
 constexpr float kPScale = 8.0f;    // weights are held times 2^8
 constexpr float kLoScale = 32.0f;  // low parts, of queries too, times 2^5 more
+// A row's score scale is at least this: 0 times the -inf of a masked position would be
+// NaN (a product of 2^24 at most times this is still nothing).
+constexpr float kMinScale = 0x1p-126f;
 // log2: sums stay below 2^(8 + 25 + 64), outputs below 2^9 times that
 constexpr float kFarBelow = 64.0f;
 
@@ -623,8 +626,9 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 *reinterpret_cast<uint2 *>(dst + off) = hi;
                 *reinterpret_cast<uint2 *>(dst + NR * kDim + off) = lo;
                 if (sub == 0) {
-                    row_scale[rb + r] =
-                        a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+                    row_scale[rb + r] = fmaxf(
+                        a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23),
+                        kMinScale);
                     row_lim[rb + r] = a.causal
                                           ? min(cur.seq.len - cur.seq.q_real + r / G, cur.seq.len - 1)
                                           : cur.seq.len - 1;

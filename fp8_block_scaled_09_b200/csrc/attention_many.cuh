@@ -755,8 +755,9 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 for (int c = 0; c < 16; ++c) top = max(top, amax_bits8(*staged(lane, c)));
                 const int e = max(static_cast<int>(top >> 7) - 127, -100);
                 const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
-                const float scale =
-                    a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+                const float scale = fmaxf(
+                    a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23),
+                    kMinScale);
                 // Parts of 16 channels take the places of their row's 16-byte pieces c and
                 // 8 + c, so the first 8 pieces move to registers and the last go first.
                 uint4 u[8];
