@@ -340,7 +340,8 @@ FP8BQ_API fp8bq_status fp8bq_rope_kv_write_e4m3(
  * the same run of at most 1920 positions if that is more.  Above 16: queries exact
  * down to 2^-9 and within 2^-17; weights within 2^-11, or 2^-32 of the row's largest.
  * Slots at or behind a sequence's length may hold anything, NaN codes too;
- * the cache positions that a sequence has must hold finite values, and q too.
+ * the cache positions that a sequence has must hold finite values, and q too,
+ * with |z_c| below 2^21 (an FP32 score of that size is off by 0.1 as it is).
  * Rows of q and out at or behind cu_q[B] are padding: neither read nor written.
  * What the host cannot see is checked on the device, without a fault, and
  * reported as FP8BQ_ERR_INDEX through fp8bq_last_device_status: a page outside
