@@ -48,7 +48,7 @@ OP_GEMM = 0
 OP_LINEAR = 1
 OP_GEMM_SILU = 2
 HEAD_DIM = 128  # channels of a head in paged_attention
-ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "yarn_exact": 4}
 
 STATUS_NAMES = {
     0: "FP8BQ_OK", 1: "FP8BQ_ERR_INVALID_ARG", 2: "FP8BQ_ERR_UNSUPPORTED_SHAPE",
@@ -509,7 +509,8 @@ def rope_inv_freq(rot_dim: int, base: float, scaling: str = "plain", factor: flo
                   old_context: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
                   device=None) -> tuple[torch.Tensor, float]:
     """fp8bq_rope_inv_freq: (FP32 frequencies [rot_dim / 2] on `device`, factor on cos and sin).
-    scaling: "plain", "linear", "ntk" or "yarn" ("yarn" also needs old_context)."""
+    scaling: "plain", "linear", "ntk", "yarn" or "yarn_exact" (both also need old_context;
+    "yarn" rounds the ends of its ramp to whole pairs, as checkpoints have it)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
     f = torch.empty(max(0, int(rot_dim) // 2), dtype=torch.float32)

@@ -941,27 +941,41 @@ fp8bq_status fp8bq_rope_inv_freq(int64_t rot_dim, double base, fp8bq_rope_scalin
                                  double beta_slow, float *inv_freq, float *mscale) {
     if (rot_dim <= 0 || rot_dim % 2 != 0 || rot_dim > kMaxDim) return FP8BQ_ERR_UNSUPPORTED_SHAPE;
     if (!inv_freq || !mscale || !(base > 1.0) || std::isinf(base)) return FP8BQ_ERR_INVALID_ARG;
-    if (scaling < FP8BQ_ROPE_PLAIN || scaling > FP8BQ_ROPE_YARN) return FP8BQ_ERR_INVALID_ARG;
+    if (scaling < FP8BQ_ROPE_PLAIN || scaling > FP8BQ_ROPE_YARN_EXACT) return FP8BQ_ERR_INVALID_ARG;
+    const bool yarn = scaling == FP8BQ_ROPE_YARN || scaling == FP8BQ_ROPE_YARN_EXACT;
     if (scaling != FP8BQ_ROPE_PLAIN && (!(factor >= 1.0) || std::isinf(factor)))
         return FP8BQ_ERR_INVALID_ARG;
-    if (scaling == FP8BQ_ROPE_YARN && (!(old_context > 0.0) || std::isinf(old_context) ||
-                                       !(beta_slow > 0.0) || !(beta_fast > beta_slow) ||
-                                       std::isinf(beta_fast)))
+    if (yarn && (!(old_context > 0.0) || std::isinf(old_context) || !(beta_slow > 0.0) ||
+                 !(beta_fast > beta_slow) || std::isinf(beta_fast)))
         return FP8BQ_ERR_INVALID_ARG;
     const double R = static_cast<double>(rot_dim);
     if (scaling == FP8BQ_ROPE_NTK && rot_dim > 2) base *= std::pow(factor, R / (R - 2.0));
+    // YaRN: the pair (a real number) that turns `turns` times in the old context, where
+    // old_context base^(-2 pair / R) = 2 pi turns; between the two ends frequencies
+    // go over from f to f / factor, linearly in the pair's number
+    double first = 0.0, last = 0.0;
+    if (yarn) {
+        const auto pair_of = [&](double turns) {
+            return 0.5 * R * std::log(old_context / (6.283185307179586477 * turns)) / std::log(base);
+        };
+        first = pair_of(beta_fast);
+        last = pair_of(beta_slow);
+        if (scaling == FP8BQ_ROPE_YARN) {
+            first = std::min(std::max(std::floor(first), 0.0), R - 1.0);
+            last = std::min(std::max(std::ceil(last), 0.0), R - 1.0);
+            if (last <= first) last = first + 0.001;
+        }
+    }
     for (int64_t i = 0; i < rot_dim / 2; ++i) {
         double f = std::pow(base, -2.0 * static_cast<double>(i) / R);
         if (scaling == FP8BQ_ROPE_LINEAR) f /= factor;
-        if (scaling == FP8BQ_ROPE_YARN) {
-            const double turns = old_context * f / 6.283185307179586477;
-            const double keep = std::min(1.0, std::max(0.0, std::log(turns / beta_slow) /
-                                                                std::log(beta_fast / beta_slow)));
-            f = f * keep + f / factor * (1.0 - keep);
+        if (yarn) {
+            const double slowed = std::min(1.0, std::max(0.0, (static_cast<double>(i) - first) / (last - first)));
+            f = f * (1.0 - slowed) + f / factor * slowed;
         }
         inv_freq[i] = static_cast<float>(f);
     }
-    *mscale = scaling == FP8BQ_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    *mscale = yarn ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
     return FP8BQ_OK;
 }
 

@@ -255,17 +255,20 @@ typedef enum {
     FP8BQ_ROPE_PLAIN = 0,  /* f_i = base^(-2i/rot_dim) */
     FP8BQ_ROPE_LINEAR = 1, /* f_i / factor (positions interpolated) */
     FP8BQ_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) */
-    FP8BQ_ROPE_YARN = 3    /* f_i / factor for pairs that turn at most beta_slow times in
-                              old_context, f_i for those that turn beta_fast times or more,
-                              linear in the logarithm of the turns between; cos and sin times
+    FP8BQ_ROPE_YARN = 3,   /* f_i up to the pair that turns beta_fast times in old_context, rounded
+                              down, f_i / factor from the pair that turns beta_slow times,
+                              rounded up, linear in i between; both ends within
+                              [0, rot_dim - 1], at least 0.001 apart.  This is what YaRN
+                              checkpoints are trained and served with.  cos and sin times
                               0.1 ln(factor) + 1 */
+    FP8BQ_ROPE_YARN_EXACT = 4 /* the same with both ends as they are, not rounded */
 } fp8bq_rope_scaling;
 
 /*
  * Host helper: fills inv_freq[rot_dim / 2] (host memory) with the FP32 rotary
  * frequencies and *mscale with the factor on cosine and sine.  factor >= 1 is
  * used by every scaling but PLAIN; old_context, beta_fast > beta_slow > 0 by
- * YARN only.  A user with another schedule fills the table itself.
+ * the two YARN ones only.  A user with another schedule fills the table itself.
  */
 FP8BQ_API fp8bq_status fp8bq_rope_inv_freq(int64_t rot_dim, double base, fp8bq_rope_scaling scaling,
                                            double factor, double old_context, double beta_fast,
