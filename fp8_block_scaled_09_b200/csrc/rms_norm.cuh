@@ -9,7 +9,7 @@
 // h would round every value twice), only its optional BF16 copy is.
 //
 // The row's factor cancels in the codes: with p = r w, exact in FP32 (two BF16
-// factors), h / s = 448 p / amax(|p|), where 448 p is exact too (7 p and a power
+// factors; below 2^-126 to FP32's smallest step), h / s = 448 p / amax(|p|), where 448 p is exact too (7 p and a power
 // of two), so a code is E4M3 of one correctly rounded quotient.  The codes
 // therefore do not wait for the sum of squares; only scales and h do.
 //
@@ -63,11 +63,15 @@ __device__ __forceinline__ uint2 encode8_of_max(const float (&p)[8], float top) 
             e[j] = e4m3x2_satfinite(corrected_quotient(448.0f * p[2 * j], top, y),
                                     corrected_quotient(448.0f * p[2 * j + 1], top, y));
     } else {
-        // where 448 p or the quotient's residual may leave the normal range
-        const float scale = top == 0.0f ? 1.0f : __fdiv_rn(top, 448.0f);
+        // Where 448 p or the quotient's residual may leave the normal range: p and top
+        // times a power of two, which is exact wherever the code is not 0 and leaves the
+        // quotient as it is.  (top / 448 itself may be subnormal, or 0.)
+        const float shift = top < 1.0f ? 0x1p70f : 0x1p-70f;
+        const float t = top == 0.0f ? 1.0f : top * shift, y = __frcp_rn(t);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            e[j] = e4m3x2_satfinite(__fdiv_rn(p[2 * j], scale), __fdiv_rn(p[2 * j + 1], scale));
+            e[j] = e4m3x2_satfinite(corrected_quotient(448.0f * (p[2 * j] * shift), t, y),
+                                    corrected_quotient(448.0f * (p[2 * j + 1] * shift), t, y));
     }
     return make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
 }

@@ -240,7 +240,9 @@ FP8BQ_API fp8bq_status fp8bq_gemm_silu_mul_quantize(const uint8_t *qa, const flo
  *                       is; may be the same buffer as residual_bf16 or x_bf16
  *   q_e4m3, s         : out, codes [M, K] and scales [M, K/128]; both or neither
  *   h_bf16            : out, optional BF16 [M, K], BF16(h); required without q_e4m3
- * The sum of squares is FP32: |r| below 2^60.
+ * The sum of squares is FP32: |r| and |weight| below 2^60, and a row whose root mean
+ * square is below 2^-50 needs eps >= 2^-100 (without it an all-zero row has no h; its
+ * codes are 0).
  * K a multiple of 128, at most 32768; eps >= 0 and finite.  Other than the
  * aliasing named above, buffers must not overlap.
  */
