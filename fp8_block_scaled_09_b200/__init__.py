@@ -40,7 +40,7 @@ __all__ = [
     "LIB_PATH", "kv_write_e4m3", "silu_mul_quantize", "gemm_silu_mul_quantize",
     "nvfp4_quantize_weight", "nvfp4_gemm_a16", "rms_norm_quantize", "rms_norm", "rope_inv_freq",
     "rope_kv_write_e4m3", "paged_attention", "attention_workspace_size", "new_attention_workspace",
-    "HEAD_DIM",
+    "HEAD_DIM", "WORKSPACE_HEADER",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8bq.so")
@@ -48,6 +48,7 @@ OP_GEMM = 0
 OP_LINEAR = 1
 OP_GEMM_SILU = 2
 HEAD_DIM = 128  # channels of a head in paged_attention
+WORKSPACE_HEADER = 16384  # bytes of counters at the start of every workspace
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "yarn_exact": 4}
 
 STATUS_NAMES = {
@@ -577,9 +578,12 @@ def attention_workspace_size(T: int, B: int, q_heads: int, kv_heads: int, max_q_
 
 def new_attention_workspace(T: int, B: int, q_heads: int, kv_heads: int, max_q_len: int,
                             device) -> torch.Tensor:
-    """A zero-filled (initial-state) workspace for paged_attention of this batch."""
-    return torch.zeros(max(attention_workspace_size(T, B, q_heads, kv_heads, max_q_len), 256),
-                       dtype=torch.uint8, device=device)
+    """A workspace in its initial state for paged_attention of this batch: the counters at its
+    start are zero, the rest (up to 42 MB) is as it was allocated."""
+    ws = torch.empty(max(attention_workspace_size(T, B, q_heads, kv_heads, max_q_len), 256),
+                     dtype=torch.uint8, device=device)
+    ws[:WORKSPACE_HEADER].zero_()
+    return ws
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -593,7 +597,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     BF16 [T, q_heads 128].  Sequence b has rows cu_q[b] .. cu_q[b+1] - 1 of q, seq_lens[b] cache
     positions (its new tokens' among them) and pages page_table[b] (int32 [B, max_pages]; rows
     may be strided); seq_lens int32 [B], cu_q int32 [B + 1].  scale defaults to 128^-1/2.  Pass
-    lse (FP32 [T, q_heads]) to also receive the log of the softmax's denominator.  Out-of-range
+    lse (FP32 [T, q_heads]) to also receive the log of the softmax's denominator.  Without a
+    workspace (new_attention_workspace) each call makes its own.  Out-of-range
     pages and lengths are reported through last_device_status()."""
     dev = _first(q, "q")
     T, width = q.shape[0], q_heads * HEAD_DIM
