@@ -422,13 +422,13 @@ def _dense(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int, name: st
 
 
 def _rows(t: torch.Tensor, cols: int, rows: int, dev: int, name: str) -> int:
-    """Row stride of a BF16 [rows, cols] tensor with unit column stride."""
+    """Row stride of a BF16 [rows, cols] tensor with unit column stride.  A single row may have any."""
     if t.dtype is not torch.bfloat16 or t.shape != (rows, cols) or t.get_device() != dev:
         _refuse(t, torch.bfloat16, (rows, cols), dev, name)
     step, unit = t.stride()
     if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return step if rows > 1 else max(step, cols)
+    return step if rows > 1 or (step >= cols and step % 8 == 0) else cols
 
 
 def _first(t: torch.Tensor, name: str) -> int:
@@ -566,6 +566,8 @@ def rope_kv_write_e4m3(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: tor
     if q_out is None:
         q_out = torch.empty((T, q_heads * head_dim), dtype=torch.bfloat16, device=qkv.device)
     out_step = _rows(q_out, q_heads * head_dim, T, dev, "q_out")
+    if T == 1 and q_out.data_ptr() == qkv.data_ptr():  # in place, whatever the row's stride
+        out_step = step
     _call(dev, (_lib or lib()).fp8bq_rope_kv_write_e4m3, qkv.data_ptr(), step, T, q_heads, kv_heads,
           head_dim, pp, pf, 2 * pairs, 1 if interleaved else 0, mscale, pl, q_out.data_ptr(), out_step,
           pk, pv, slots, slot_bytes)
