@@ -268,10 +268,21 @@ static_assert(sizeof(Segment) == 64, "shared-memory layout");
 struct SegReader {
     uint64_t *full, *empty;
     const Segment *ring;
+    const volatile int *stopped;  // place of the first segment that will not come, or -1
     uint32_t i, phase;
 
+    __device__ static int place(uint32_t i, uint32_t phase) { return static_cast<int>(i | (phase << 8)); }
     __device__ const Segment *next(volatile int *abort_flag, int *status) const {
         if (!mbar_wait(&full[i], phase, abort_flag, status)) return nullptr;
+        return ring[i].valid ? ring + i : nullptr;
+    }
+    // For warps that meet at named barriers and therefore have to take the same segments,
+    // behind a wait that gave up too: ends only where the work list's warp stopped.
+    // That warp either publishes or stops, since its own wait is bounded, and at most
+    // kSegs segments lie between it and a reader, so a place stands for one segment.
+    __device__ const Segment *next_published() const {
+        while (!mbar_try_wait(&full[i], phase))
+            if (*stopped == place(i, phase)) return nullptr;
         return ring[i].valid ? ring + i : nullptr;
     }
     // Warp-wide: this warp is done with the current one.
@@ -310,6 +321,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
     int *parts = reinterpret_cast<int *>(misc + 7);            // CTAs that have a part
     int64_t *start_w = reinterpret_cast<int64_t *>(misc + 8);  // w0, w1, base, total
     int64_t *warp_cost = start_w + 4;                          // [16]
+    volatile int *seg_stopped = reinterpret_cast<volatile int *>(warp_cost + 16);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     allow_dependent_launch();
@@ -331,6 +343,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(&segempty[i], kSegUsers);
         }
         *abort_flag = 0;
+        *seg_stopped = -1;
         fence_barrier_init();
         prefetch_tmap(&tmap_k);
         prefetch_tmap(&tmap_v);
@@ -402,7 +415,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    SegReader segs{segfull, segempty, seg_ring, 0, 0};
+    SegReader segs{segfull, segempty, seg_ring, seg_stopped, 0, 0};
 
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
@@ -474,7 +487,10 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 uint32_t i = 0, phase = 0;
                 for (bool more = true; more;) {
                     more = it.next();
-                    if (!mbar_wait(&segempty[i], phase ^ 1, abort_flag, status)) break;
+                    if (!mbar_wait(&segempty[i], phase ^ 1, abort_flag, status)) {
+                        *seg_stopped = SegReader::place(i, phase);
+                        break;
+                    }
                     Segment &sg = seg_ring[i];
                     sg.valid = more;
                     if (more) {
@@ -702,8 +718,9 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ------------------------------------------------------------ softmax
-        // A wait that gives up sets the abort flag: the loops then run to their
-        // end without waiting, so that every barrier still has all its warps.
+        // A wait that gives up sets the abort flag: the loops then run without
+        // waiting through every segment that was published, so that every barrier still has
+        // all its warps.
         const int half = warp >> 2, ht = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_tm = tmem + lanes + F::s_col(half), o_tm = tmem + lanes + F::o_col(half);
@@ -721,7 +738,7 @@ attention_many_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // the product and the scores issued before them.
         const bool releases = (warp & 3) == 0 && lane == 0;
         for (;; segs.release()) {
-            const Segment *sg = segs.next(abort_flag, status);
+            const Segment *sg = segs.next_published();
             if (sg == nullptr) break;
             const int n = sg->count[half];
             const bool dual = sg->dual;
