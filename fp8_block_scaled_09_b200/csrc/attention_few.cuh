@@ -603,7 +603,7 @@ attention_few_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         static_cast<int64_t>(cur.hk * G + g) * kDim + sub * 8);
                 }
             }
-            ok = mbar_wait(&qempty[segs & 1], ((segs >> 1) & 1) ^ 1, abort_flag, status);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&qempty[segs & 1], ((segs >> 1) & 1) ^ 1, abort_flag, status));
             uint8_t *dst = smem + F::kQOff + (segs & 1) * F::kQ;
             // not unrolled (the rows move down the array instead): unrolled, the
             // first pass over this code fetched it for 4 us before the first MMA

@@ -51,3 +51,12 @@ def test_softmax_warps_of_the_few_row_kernel_end_by_the_work_list():
     softmax = text[text.index("float l_run[NR];"):text.rindex("__syncthreads()")]
     loop = body(softmax, "while (cur.next())")
     assert "named_barrier(" in loop and "break;" not in loop and "return;" not in loop
+
+
+def test_the_query_warp_of_the_few_row_kernel_leaves_as_a_whole():
+    """Its loop shuffles with every lane."""
+    text = source("attention_few.cuh")
+    loop = body(text[text.index("const int sub = lane & 15"):], "while (ok && cur.next())")
+    assert "__shfl_xor_sync(0xFFFFFFFFu" in loop
+    assert re.findall(r"\bok = [^;]*;", loop) == \
+        ["ok = __all_sync(0xFFFFFFFFu, mbar_wait(&qempty[segs & 1], ((segs >> 1) & 1) ^ 1, abort_flag, status));"]
