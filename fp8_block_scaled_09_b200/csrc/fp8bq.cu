@@ -108,7 +108,9 @@ struct DeviceInfo {
 };
 
 DeviceInfo g_dev[kMaxDevices];
-std::once_flag g_dev_once[kMaxDevices];
+// Set once a device's set-up has an answer; one that failed is tried again by the next call.
+std::atomic<bool> g_dev_done[kMaxDevices];
+std::mutex g_dev_mu;
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -156,131 +158,148 @@ bool prefill_variant_ready() {
            prefill_instance_ready<kSilu>(prefill::gemm_prefill_kernel<kPrefillBN, kSilu, 32>);
 }
 
+// Fills in a device's info; false where a call failed.  The status word is zero from its
+// definition.
+bool set_up_device(int dev, DeviceInfo &d) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return false;
+    if (major != 10 || minor != 0) return true;  // built for sm_100a only
+    if (cudaGetSymbolAddress(reinterpret_cast<void **>(&d.status), g_status) != cudaSuccess)
+        return false;
+    // The prefill kernel moves registers between warpgroups with setmaxnreg;
+    // the split is only safe if the launch allocates exactly what it was
+    // designed for (otherwise setmaxnreg.inc could wait forever).
+    cudaFuncAttributes fa;
+    if (!prefill_variant_ready<false>() || !prefill_variant_ready<true>()) return false;
+    // CTA-pair prefill kernel: optional; any failure here only leaves it off.
+    d.pair_clusters = 0;
+    if (pair_prefill_requested() &&
+        cudaFuncSetAttribute(prefill2::gemm_prefill_pair_kernel,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             prefill2::Layout::kDynamicSmem) == cudaSuccess &&
+        cudaFuncGetAttributes(&fa, prefill2::gemm_prefill_pair_kernel) == cudaSuccess &&
+        fa.numRegs == prefill2::kLaunchRegs) {
+        // how many 2-CTA clusters fit at once: the persistent pair grid size
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (d.sm_count / 2));
+        cfg.blockDim = dim3(prefill2::kNumThreads);
+        cfg.dynamicSmemBytes = prefill2::Layout::kDynamicSmem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&d.pair_clusters, prefill2::gemm_prefill_pair_kernel,
+                                           &cfg) != cudaSuccess)
+            d.pair_clusters = 0;
+        cudaGetLastError();  // clear a failed query
+    }
+    if (cudaFuncSetAttribute(quantize_act_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ActLayout::kBytes) != cudaSuccess)
+        return false;
+    if (cudaFuncSetAttribute(decode::gemm_decode_kernel<16>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             decode::kMaxSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(decode::gemm_decode_kernel<32>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             decode::kMaxSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(decode::gemm_decode_kernel<64>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             decode::kMaxSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(decode::gemm_decode_kernel<128>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             decode::kMaxSmem) != cudaSuccess)
+        return false;
+    // How many clusters of decode CTAs (one per SM at full shared memory)
+    // the GPU can hold at once, per cluster size.
+    for (int c = 2; c <= 8; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(c));
+        cfg.blockDim = dim3(decode::Roles<128>::kNumThreads);
+        cfg.dynamicSmemBytes = decode::kMaxSmem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = static_cast<unsigned>(c);
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, decode::gemm_decode_kernel<128>, &cfg) != cudaSuccess)
+            n = 0;
+        cudaGetLastError();  // clear a failed query
+        d.cluster_capacity[c] = n;
+    }
+    if (cudaFuncSetAttribute(nvfp4::nvfp4_gemm_a16_kernel,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             nvfp4::Layout::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(nvfp4::nvfp4_gemv_a16_kernel<1>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             nvfp4::GemvLayout<1>::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(nvfp4::nvfp4_gemv_a16_kernel<2>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             nvfp4::GemvLayout<2>::kBytes) != cudaSuccess)
+        return false;
+    if (cudaFuncSetAttribute(attn::attention_few_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::Few<16>::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::attention_few_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::Few<8>::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::attention_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::Many::kBytes) != cudaSuccess)
+        return false;
+    // the register split (setmaxnreg) assumes this launch allocation
+    if (cudaFuncGetAttributes(&fa, attn::attention_many_kernel) != cudaSuccess ||
+        fa.numRegs != attn::kManyLaunchRegs)
+        return false;
+    for (int c = 2; c <= 8; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(c));
+        cfg.blockDim = dim3(nvfp4::kNumThreads);
+        cfg.dynamicSmemBytes = nvfp4::Layout::kBytes;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = static_cast<unsigned>(c);
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, nvfp4::nvfp4_gemm_a16_kernel, &cfg) != cudaSuccess)
+            n = 0;
+        cudaGetLastError();
+        d.nvfp4_cluster_capacity[c] = n;
+    }
+    d.supported = true;
+    return true;
+}
+
+// The set-up may run inside a stream capture, if that holds the device's first
+// call: it enqueues nothing, and loading the kernels is allowed to a thread in relaxed mode.
+struct RelaxedCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 // Current device's info, set up once per device (kernel attributes, status word).
 const DeviceInfo *device_info() {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-    std::call_once(g_dev_once[dev], [dev] {
-        DeviceInfo &d = g_dev[dev];
-        int major = 0, minor = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return;
-        if (major != 10 || minor != 0) return;  // built for sm_100a only
-        if (cudaGetSymbolAddress(reinterpret_cast<void **>(&d.status), g_status) != cudaSuccess)
-            return;
-        if (cudaMemset(d.status, 0, sizeof(int)) != cudaSuccess) return;
-        // The prefill kernel moves registers between warpgroups with setmaxnreg;
-        // the split is only safe if the launch allocates exactly what it was
-        // designed for (otherwise setmaxnreg.inc could wait forever).
-        cudaFuncAttributes fa;
-        if (!prefill_variant_ready<false>() || !prefill_variant_ready<true>()) return;
-        // CTA-pair prefill kernel: optional; any failure here only leaves it off.
-        d.pair_clusters = 0;
-        if (pair_prefill_requested() &&
-            cudaFuncSetAttribute(prefill2::gemm_prefill_pair_kernel,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 prefill2::Layout::kDynamicSmem) == cudaSuccess &&
-            cudaFuncGetAttributes(&fa, prefill2::gemm_prefill_pair_kernel) == cudaSuccess &&
-            fa.numRegs == prefill2::kLaunchRegs) {
-            // how many 2-CTA clusters fit at once: the persistent pair grid size
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(2 * (d.sm_count / 2));
-            cfg.blockDim = dim3(prefill2::kNumThreads);
-            cfg.dynamicSmemBytes = prefill2::Layout::kDynamicSmem;
-            cudaLaunchAttribute at[1];
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim.x = 2;
-            at[0].val.clusterDim.y = 1;
-            at[0].val.clusterDim.z = 1;
-            cfg.attrs = at;
-            cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&d.pair_clusters, prefill2::gemm_prefill_pair_kernel,
-                                               &cfg) != cudaSuccess)
-                d.pair_clusters = 0;
-            cudaGetLastError();  // clear a failed query
+    if (!g_dev_done[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lk(g_dev_mu);
+        if (!g_dev_done[dev].load(std::memory_order_relaxed)) {
+            RelaxedCapture relaxed;
+            if (set_up_device(dev, g_dev[dev])) g_dev_done[dev].store(true, std::memory_order_release);
+            cudaGetLastError();  // of a failed set-up: the caller gets a status
         }
-        if (cudaFuncSetAttribute(quantize_act_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 ActLayout::kBytes) != cudaSuccess)
-            return;
-        if (cudaFuncSetAttribute(decode::gemm_decode_kernel<16>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 decode::kMaxSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(decode::gemm_decode_kernel<32>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 decode::kMaxSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(decode::gemm_decode_kernel<64>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 decode::kMaxSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(decode::gemm_decode_kernel<128>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 decode::kMaxSmem) != cudaSuccess)
-            return;
-        // How many clusters of decode CTAs (one per SM at full shared memory)
-        // the GPU can hold at once, per cluster size.
-        for (int c = 2; c <= 8; ++c) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(static_cast<unsigned>(c));
-            cfg.blockDim = dim3(decode::Roles<128>::kNumThreads);
-            cfg.dynamicSmemBytes = decode::kMaxSmem;
-            cudaLaunchAttribute at[1];
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim.x = static_cast<unsigned>(c);
-            at[0].val.clusterDim.y = 1;
-            at[0].val.clusterDim.z = 1;
-            cfg.attrs = at;
-            cfg.numAttrs = 1;
-            int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, decode::gemm_decode_kernel<128>, &cfg) != cudaSuccess)
-                n = 0;
-            cudaGetLastError();  // clear a failed query
-            d.cluster_capacity[c] = n;
-        }
-        if (cudaFuncSetAttribute(nvfp4::nvfp4_gemm_a16_kernel,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 nvfp4::Layout::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(nvfp4::nvfp4_gemv_a16_kernel<1>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 nvfp4::GemvLayout<1>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(nvfp4::nvfp4_gemv_a16_kernel<2>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 nvfp4::GemvLayout<2>::kBytes) != cudaSuccess)
-            return;
-        if (cudaFuncSetAttribute(attn::attention_few_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 attn::Few<16>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(attn::attention_few_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 attn::Few<8>::kBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(attn::attention_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 attn::Many::kBytes) != cudaSuccess)
-            return;
-        // the register split (setmaxnreg) assumes this launch allocation
-        if (cudaFuncGetAttributes(&fa, attn::attention_many_kernel) != cudaSuccess ||
-            fa.numRegs != attn::kManyLaunchRegs)
-            return;
-        for (int c = 2; c <= 8; ++c) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(static_cast<unsigned>(c));
-            cfg.blockDim = dim3(nvfp4::kNumThreads);
-            cfg.dynamicSmemBytes = nvfp4::Layout::kBytes;
-            cudaLaunchAttribute at[1];
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim.x = static_cast<unsigned>(c);
-            at[0].val.clusterDim.y = 1;
-            at[0].val.clusterDim.z = 1;
-            cfg.attrs = at;
-            cfg.numAttrs = 1;
-            int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, nvfp4::nvfp4_gemm_a16_kernel, &cfg) != cudaSuccess)
-                n = 0;
-            cudaGetLastError();
-            d.nvfp4_cluster_capacity[c] = n;
-        }
-        if (cudaDeviceSynchronize() != cudaSuccess) return;
-        d.supported = true;
-    });
+    }
     const DeviceInfo *d = &g_dev[dev];
-    return d->supported ? d : nullptr;
+    return g_dev_done[dev].load(std::memory_order_acquire) && d->supported ? d : nullptr;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

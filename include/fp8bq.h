@@ -33,7 +33,8 @@
  *
  * Execution: every compute call is asynchronous on the given stream (a
  * cudaStream_t passed as void*; NULL = the legacy default stream) and returns
- * after enqueueing.  Argument errors are detected on the host before anything
+ * after enqueueing.  It may be captured into a graph, the process's first call too
+ * (but see fp8bq_gemm_noalloc).  Argument errors are detected on the host before anything
  * is enqueued and reported synchronously.  A kernel that gives up on an
  * internal wait (FP8BQ_ERR_TIMEOUT) records it in a per-device status word,
  * read by fp8bq_last_device_status().
