@@ -82,3 +82,52 @@ def test_scores_near_the_documented_limit(n):
             assert bool(((lse[at].double() - top[:, 0]).abs() <= dz + 2.0 ** -22 * top[:, 0].abs())[clear].all())
             sure, at = sure + int(clear.sum()), at + 1
     assert sure > 7 * n
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_the_longest_context(n):
+    """2^25 positions over 32 pages that come again and again: the same weights as over each of them once (the last
+    tokens' own few positions aside), and a log-sum-exp larger by the log of how often."""
+    page, pages, length = 64, 32, 1 << 25
+    c = ref.random_batch([n], [pages * page], 7, 1, page, 2, spare_pages=0)
+    o, l, bound, l_bound = ref.attention(c["q"], c["k_cache"], c["v_cache"], c["page_table"], c["seq_lens"], c["cu_q"],
+                                         page, 7, 1, 128 ** -0.5, False)
+    times = length // (pages * page)
+    long = dict(c, page_table=c["page_table"].repeat(1, times), seq_lens=torch.tensor([length], dtype=torch.int32))
+    for causal in (True, False):
+        out, lse = run(long, 7, 1, page, causal)
+        # 40 masked positions of 2^25 weigh 2^-16 at most (a weight is below 2^4 times the mean here)
+        slack = 2.0 ** -16 * c["v_cache"].view(torch.float8_e4m3fn).float().nan_to_num().abs().max() if causal else 0.0
+        assert bool(((out.double().view(o.shape) - o).abs() <= bound + slack).all())
+        assert bool(((lse.double() - l - math.log(times)).abs() <= l_bound + 2.0 ** -14).all())
+
+
+@pytest.mark.parametrize("heads,n", [((1024, 1), 1), ((1024, 1024), 1), ((1024, 1024), 3), ((1024, 64), 2), ((1023, 3), 1)])
+def test_the_most_heads(heads, n):
+    c = ref.random_batch([n, n], [130, 40], *heads, 16, 12)
+    check(c, *run(c, *heads, 16), *heads, 16)
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_the_most_sequences(n):
+    """65536 sequences, every third one empty, over a few shared pages."""
+    batch, page, pages = 65536, 8, 4
+    g = torch.Generator().manual_seed(n)
+    kc, vc = (torch.randn(pages * page, 128, generator=g).to(torch.float8_e4m3fn).view(torch.uint8).cuda() for _ in range(2))
+    table = torch.stack([torch.randperm(pages, generator=g)[:3] for _ in range(64)]).int().repeat(batch // 64, 1)
+    lens = (torch.arange(batch) % 3 * 11).int()
+    q = torch.randn(batch * n, 128, generator=g).bfloat16()
+    out = fp8bq.paged_attention(q.cuda(), kc, vc, table.cuda(), lens.cuda(), (torch.arange(batch + 1) * n).int().cuda(),
+                                page, 1, 1, n).cpu().double().view(batch, n, 128)
+    assert bool((out[::3] == 0).all())
+    k, v = ref.e4m3_values(kc.cpu()), ref.e4m3_values(vc.cpu())
+    for part in (1, 2):
+        b = torch.arange(part, batch, 3)
+        pos = torch.arange(11 * part)
+        slot = table[b].long()[:, pos // page] * page + pos % page
+        z = torch.einsum("bnd,bcd->bnc", q.double().view(batch, n, 128)[b], k[slot]) * 128 ** -0.5
+        z = z.masked_fill(pos > (11 * part - n + torch.arange(n))[:, None], -math.inf)
+        w = z.softmax(-1).nan_to_num()
+        o, size = w @ v[slot], w @ v[slot].abs()
+        # BF16, the weights' 2^-8 and an exponent off by 2^-12 (|z| below 16)
+        assert bool(((out[b] - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -11) * size + 2.0 ** -12).all())
