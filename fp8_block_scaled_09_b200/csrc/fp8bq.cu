@@ -40,6 +40,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <unordered_map>
 #include <utility>
 
@@ -421,7 +422,11 @@ bool make_tmap_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType type, i
         return false;
     std::lock_guard<std::mutex> lk(g_tmap_mu);
     if (g_tmap_cache.size() >= kTmapCacheMax) g_tmap_cache.clear();
-    g_tmap_cache.emplace(key, *map);
+    try {
+        g_tmap_cache.emplace(key, *map);
+    } catch (const std::bad_alloc &) {
+        // the map itself is there; no exception may leave a C entry point
+    }
     return true;
 }
 
