@@ -16,13 +16,12 @@
 // it stays below 256.  A BF16 query, scaled by a power of two that takes its row's
 // largest channel to [128, 256), is exact down to 2^-14 of that and off by at most
 // 2^-22 of it below.  A weight, held times a power of two that takes the chunk's
-// largest to (128, 256], has 8 bits down to 2^-15 of that and an absolute error of 2^-23
-// of 256 below.  (Without
-// the 32 the steps were 2^-17 of the largest: a first position 13 logits above
-// 32768 others of its own value near 0 took 21% off the output.)  Two MMAs into one
-// column cost more: an MMA with this few columns takes the time to read its
-// 4 KB of A, and with twice as many of them the tensor pipe was busy 1100 of 2550
-// cycles per tile.
+// largest to (128, 256], has 8 bits down to 2^-15 of that and an absolute error of
+// 2^-23 of 256 below.  (With lo unscaled and the row's maximum in the chunk's place
+// the steps were 2^-17 of the row's largest: a first position 13 logits above 32768
+// others, its value near 0, took 21% off the output.)  Two MMAs into one column cost
+// more: an MMA with this few columns takes the time to read its 4 KB of A, and with
+// twice as many of them the tensor pipe was busy 1100 of 2550 cycles per tile.
 //
 // Work is a list of tiles of 128 positions, ordered by (sequence, kv head,
 // tile), each head preceded by some tiles' worth of nothing for what
@@ -50,7 +49,7 @@
 // V behind a sequence's end.
 //
 // Measured, after a 256 MB write: 128 sequences of 2048 positions, 56 query and 8 kv
-// heads, pages of 64: 119 us, 4.5 TB/s; pages of 16: 141 us (a TMA box then brings only
+// heads, pages of 64: 120 us, 4.5 TB/s; pages of 16: 141 us (a TMA box then brings only
 // 2 KB, and an SM starts one in ~80 ns; half of the pages by cp.async instead, from two
 // more warps, took 211 us).  One sequence of 65001 positions, among others of its kind:
 // 32 us, of which 5 pass before its first tile and 4 in the join.

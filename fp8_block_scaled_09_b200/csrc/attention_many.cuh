@@ -6,8 +6,11 @@
 // tile of 128 positions:
 //     S[row, pos] = Q[row, :] . K[pos, :]      E4M3, M = N = 128, K = 128, twice
 //     O[row, ch] += P[row, :] . V[:, ch]       F16,  M = N = 128, K = 128
-// K is never converted: a BF16 query row is held as two E4M3 parts hi + lo (see
-// attention_few.cuh), two MMAs at twice the 16-bit rate.  V becomes F16 (exact, as
+// K is never converted: a BF16 query row, times a power of two that takes its largest
+// channel to [128, 256), is held as two E4M3 parts hi + lo, two MMAs into the same
+// columns at twice the 16-bit rate: exact down to 2^-9 of that channel and off by at
+// most 2^-17 of it below (parts of different scale, as in attention_few.cuh, would need
+// columns of their own, and the tensor memory is full).  V becomes F16 (exact, as
 // 2^-8 V: an E4M3 code's bits moved into an F16 are its value times 2^-8, so
 // four integer instructions convert two codes; the output takes the 2^8 back).
 // P is F16 too, 11 bits, and never leaves the tensor memory: it replaces the
@@ -38,9 +41,10 @@
 // have no registers to spare for it: walking it in every role spilled scores), warp 15
 // writes the zeros of sequences without positions.
 //
-// Measured: 2048 tokens of 56 + 8 heads at 18001 positions 811 us, 1.23 PFLOP/s (a pair
+// Measured: 2048 tokens of 56 + 8 heads at 18001 positions 821 us, 1.21 PFLOP/s (947 us in
+// a loop, under the power cap; a pair
 // of halves takes ~3400 cycles per tile where its MMAs take 2048: the softmax chain
-// between them); a prompt of 8192 tokens 885 us; 16 blocks of 8 tokens of 28 + 4
+// between them); a prompt of 8192 tokens 889 us; 16 blocks of 8 tokens of 28 + 4
 // heads at 1000 .. 8000 positions 45 us.
 #pragma once
 

@@ -724,6 +724,11 @@ cudaError_t launch_rms_norm(const DeviceInfo &d, const void *x, const void *resi
     // as there are threads for (1 x 7168 3.2 us with one, 3.8 with two; 149 x 2048 2.7
     // and 3.3; 1 x 8320 4.5 with two, 5.8 with four).  Beyond, several rows per SM in
     // flight: two vectors (2048 x 7168 21.6 us; 35.3 with one, 23.9 with four).
+    // Beyond 8192 channels two vectors only while there is a row per SM, then four: 148 x
+    // 8320 4.1 us with two, 149 x 12288 6.1 with four and 7.2 with two, 297 x 8320 6.9 and 7.2,
+    // 444 x 8320 7.7 and 8.7, 2048 x 12288 40 and 48.  (Where two rows of the two-vector
+    // kernel fit an SM, up to 8704 channels, 149 .. 296 rows would be better with two: 296 x
+    // 8320 5.4 against 6.9.)
     const int64_t vecs = K / 8;
     if (vecs <= 1024 && M <= d.sm_count * (1024 / vecs))
         return launch_rms_norm_v<1, 1024, 1>(x, residual, weight, eps, M, K, residual_out, q, s, h, st);

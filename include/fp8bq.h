@@ -299,7 +299,9 @@ FP8BQ_API fp8bq_status fp8bq_rope_inv_freq(int64_t rot_dim, double base, fp8bq_r
  * head_dim a multiple of 16 up to 256, rot_dim a multiple of 16 up to
  * head_dim, strides multiples of 8 (slot_stride of 16), at most 1024 heads of
  * each kind; qkv, q_out and the caches 16-byte, positions and loc 8-byte
- * aligned.  A token with loc -1 is padding: nothing of it is written.  Any
+ * aligned.  Distinct tokens should have distinct slots (with duplicates, which of
+ * the tokens each 8 bytes of a slot come from is unspecified).
+ * A token with loc -1 is padding: nothing of it is written.  Any
  * other slot outside [0, num_slots) skips the token too and is reported as
  * FP8BQ_ERR_INDEX through fp8bq_last_device_status.
  */
