@@ -344,7 +344,7 @@ FP8BQ_API fp8bq_status fp8bq_rope_kv_write_e4m3(
  * Scores, softmax sums and outputs are accumulated in FP32.  What multiplies K
  * and V is rounded, the sums' weights are not.  Up to 16 new tokens x heads of a
  * group: queries exact down to 2^-14 of a row's largest channel and within 2^-22 of
- * it below; weights within 2^-8 of themselves, or 2^-22 of the largest weight in
+ * it below; weights within 2^-8 of themselves, or 2^-23 of the largest weight in
  * the same run of at most 1920 positions if that is more.  Above 16: queries exact
  * down to 2^-9 and within 2^-17; weights within 2^-11, or 2^-32 of the row's largest.
  * Slots at or behind a sequence's length may hold anything, NaN codes too;
