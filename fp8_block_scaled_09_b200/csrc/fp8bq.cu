@@ -1030,7 +1030,8 @@ fp8bq_status fp8bq_rope_kv_write_e4m3(const void *qkv_bf16, int64_t row_stride, 
         return FP8BQ_ERR_UNSUPPORTED_SHAPE;
     if (num_slots > 0 && slot_stride > kMaxBytes / num_slots) return FP8BQ_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return FP8BQ_OK;
-    if (!qkv_bf16 || !positions || !inv_freq || !loc || !q_out_bf16 || !k_cache || !v_cache)
+    if (!qkv_bf16 || !positions || !inv_freq || !loc || !q_out_bf16 ||
+        (num_slots > 0 && (!k_cache || !v_cache)))  // a cache of no slots may be absent
         return FP8BQ_ERR_INVALID_ARG;
     if (q_out_bf16 == qkv_bf16 && q_stride != row_stride) return FP8BQ_ERR_INVALID_ARG;
     if (!aligned16(qkv_bf16) || !aligned16(q_out_bf16) || !aligned16(k_cache) ||
